@@ -84,8 +84,8 @@ const char* gdn_last_error_message(void);
 /*
  * Synchronises `stream`, then reads and clears the current device's error word.
  * Returns GDN_ERR_TIMEOUT if a kernel's bounded wait ran out since the last check,
- * GDN_ERR_INVALID_ARG if a kernel found cu_seqlens out of order / range or a state
- * slot out of range, GDN_ERR_CUDA if the stream reports a CUDA error, else GDN_OK.
+ * GDN_ERR_INVALID_ARG if a kernel found cu_seqlens out of order / range, a state
+ * slot out of range or a page outside the cache, GDN_ERR_CUDA if the stream reports a CUDA error, else GDN_OK.
  */
 gdn_status_t gdn_check_device_error(gdn_stream_t stream);
 
@@ -354,6 +354,129 @@ gdn_status_t gdn_out_gate(const void* y, const void* z, const float* norm_w, flo
  */
 gdn_status_t gdn_state_map_apply(const float* M, const float* B, const float* S_in, float* S_out, int rows,
                                  int dk, int dv, gdn_stream_t stream);
+
+/*
+ * The attention layer's operators
+ * -------------------------------
+ * The architecture keeps one attention layer after every third GDN mixer.  The calls below are
+ * that layer's parts: the norms and the position rotation of its queries and keys (with their
+ * gradients, and in the form that fills a paged cache), the attention of one new token per row
+ * over that cache, and the choice of the cache pages that such a token attends to.
+ *
+ * Heads.    Hq query heads and Hkv key heads, Hq a multiple of Hkv: query head h reads key head
+ *           h / (Hq / Hkv).
+ * Cache.    k_cache, v_cache [num_pages, Hkv, page_size, d], page_size a multiple of 16 up to
+ *           1024.  page_table int32 [rows, max_pages]: position p of row b is place
+ *           p % page_size of page page_table[b][p / page_size].  Rows may share pages that are only
+ *           read.  max_pages * page_size is at most 2^30.  lens int32 [rows]: a row's keys are
+ *           positions 0 .. lens[b] - 1; what the pages hold behind them is never read.
+ * Errors.   A table entry outside [0, num_pages), a position or length beyond the table, or a
+ *           listed page beyond the row's length is skipped and flagged in the device error word
+ *           (gdn_check_device_error then returns GDN_ERR_INVALID_ARG).
+ * Workspace. A workspace serves one call at a time: calls that may overlap on the GPU (two streams,
+ *           two graphs) need one each.
+ */
+
+/*
+ * gdn_attn_prep -- per (token, head) row x of d channels, the zero-centred RMSNorm and the
+ * rotation of its first rot_dim channels in pairs (i, i + rot_dim / 2):
+ *   n_i = x_i / sqrt(mean_j x_j^2 + eps) * (1 + w_i),   theta_i = positions[t] * inv_freq[i]
+ *   y_i = n_i cos theta_i - n_{i+rot_dim/2} sin theta_i     (i < rot_dim / 2)
+ *   y_{i+rot_dim/2} = n_{i+rot_dim/2} cos theta_i + n_i sin theta_i
+ * and y_i = n_i for i >= rot_dim.
+ *   q [N,Hq,d], k [N,Hkv,d]: in_dtype; a token's heads contiguous, tokens q_stride and k_stride
+ *     elements apart (multiples of 8), so both may be slices of one projection's output.
+ *   w_q, w_k [d] fp32.  positions int32 [N].  inv_freq [rot_dim / 2] fp64, radians per position
+ *     (angles are reduced in fp64); rot_dim a multiple of 16 up to d, 0: no rotation (inv_freq may
+ *     be NULL).  d in {16,32,64,128,256}.
+ *   q_out [N,Hq,d], k_out [N,Hkv,d]: out_dtype, contiguous.  They overlap no input, except that
+ *     q_out may be q and k_out may be k when those are contiguous and of the same dtype.
+ */
+gdn_status_t gdn_attn_prep(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const float* w_q,
+                           const float* w_k, float eps, const int32_t* positions, const double* inv_freq, int rot_dim,
+                           int N, int Hq, int Hkv, int d, gdn_dtype_t in_dtype, gdn_dtype_t out_dtype, void* q_out,
+                           void* k_out, gdn_stream_t stream);
+
+/*
+ * gdn_attn_prep_cache -- gdn_attn_prep for serving: the rotated keys and the values (as they are,
+ * rounded to out_dtype) go to the cache, at each token's position in its sequence's pages.
+ *   v [N,Hkv,d] in_dtype, tokens v_stride elements apart.  cu_seqlens, num_seqs: as everywhere
+ *     (NULL: N / num_seqs tokens each, so one token per row for a decode step); sequence b's pages are
+ *     row b of page_table.
+ *   q_out [N,Hq,d], k_cache, v_cache: out_dtype (BF16 or F16; F32 returns GDN_ERR_UNSUPPORTED).
+ * A token with a negative position is padding, a token at index >= cu_seqlens[num_seqs] is in no
+ * sequence: neither has anything written, in q_out or in the caches.  Two tokens of a call must not
+ * have the same place in the cache.
+ */
+gdn_status_t gdn_attn_prep_cache(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                 int64_t v_stride, const float* w_q, const float* w_k, float eps,
+                                 const int32_t* positions, const double* inv_freq, int rot_dim,
+                                 const int32_t* cu_seqlens, int num_seqs, int N, int Hq, int Hkv, int d,
+                                 const int32_t* page_table, int max_pages, int num_pages, int page_size,
+                                 gdn_dtype_t in_dtype, gdn_dtype_t out_dtype, void* q_out, void* k_cache, void* v_cache,
+                                 gdn_stream_t stream);
+
+/*
+ * gdn_attn_prep_bwd -- gradients of gdn_attn_prep: for dq_out = dL/dq_out, dk_out = dL/dk_out (dy_dtype,
+ * contiguous) and the forward's own inputs, with dn the rotation by -theta of dy, u = x r and
+ * r = (mean_j x_j^2 + eps)^(-1/2):
+ *   dx_i = r ((1 + w_i) dn_i - u_i mean_j((1 + w_j) dn_j u_j)),   dw_i = sum_{t,h} dn_i u_i.
+ *   dq [N,Hq,d], dk [N,Hkv,d]: in_dtype, contiguous.  dw_q, dw_k [d] fp32 (zeros for N = 0).  The sums
+ *   run in a fixed order: equal calls on one kind of GPU give equal bits.  Outputs overlap no input.
+ * workspace: at least gdn_attn_prep_bwd_workspace_size(d) bytes.
+ */
+size_t gdn_attn_prep_bwd_workspace_size(int d);
+
+gdn_status_t gdn_attn_prep_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, int64_t q_stride,
+                               int64_t k_stride, const float* w_q, const float* w_k, float eps,
+                               const int32_t* positions, const double* inv_freq, int rot_dim, int N, int Hq, int Hkv,
+                               int d, gdn_dtype_t in_dtype, gdn_dtype_t dy_dtype, void* dq, void* dk, float* dw_q,
+                               float* dw_k, void* workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * gdn_attn_decode -- softmax attention of one new token per row over the row's cached keys j:
+ *   s_j = scale q . k_j,   y = sum_j e^(s_j) v_j / sum_j e^(s_j)      (per query head)
+ *   q [B,Hq,d], k_cache, v_cache: dtype (BF16 or F16).  y [B,Hq,d]: y_dtype.  d in {32,64,128,256}.
+ *   pages int32 [B,Hkv,n_sel] or NULL: the logical pages of the row that each key head attends to, negative
+ *     entries skipped, in any order (a page listed twice counts twice); NULL: all of the row.
+ * A row without a key (length 0, or no listed page) gives zeros.  Cached values are finite: an infinite one
+ * may give NaN.  fp32 scores, weights and sums; the weights enter the product with the values as a 16-bit value
+ * plus its 16-bit remainder.  Results do not depend on timing, and the same call gives the same bits.
+ * workspace: at least gdn_attn_decode_workspace_size(Hq, Hkv, d) bytes, whatever B and the lengths are; nothing
+ * in it has to be cleared.  Other head sizes and F32 return GDN_ERR_UNSUPPORTED.
+ */
+size_t gdn_attn_decode_workspace_size(int Hq, int Hkv, int d);
+
+gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                             const int32_t* lens, const int32_t* pages, int n_sel, int B, int Hq, int Hkv, int d,
+                             int max_pages, int num_pages, int page_size, float scale, gdn_dtype_t dtype,
+                             gdn_dtype_t y_dtype, void* y, void* workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * gdn_attn_page_mean -- keeps up the mean key of the pages that new tokens touched: for every page of row b
+ * that holds a position in [starts[b], lens[b]) (starts int32 [B], NULL: 0),
+ *   page_mean[page][hk][:] = mean of the page's keys at positions below lens[b]
+ * page_mean [num_pages, Hkv, d] fp32; the other pages' rows are left as they are.  k_cache, d as in
+ * gdn_attn_decode.
+ */
+gdn_status_t gdn_attn_page_mean(const void* k_cache, const int32_t* page_table, const int32_t* lens,
+                                const int32_t* starts, int B, int Hkv, int d, int max_pages, int num_pages,
+                                int page_size, gdn_dtype_t dtype, float* page_mean, gdn_stream_t stream);
+
+/*
+ * gdn_attn_select -- for each row and key head the n_sel pages that its new token attends to:
+ *   score_p = max over the query heads h of the key head's group of q_h . page_mean[p]      (fp64)
+ * The first n_first and the last n_last pages are always among them (n_first + n_last <= n_sel), the others by
+ * score, ties to the lower page; a NaN score is the lowest.  A row of at most n_sel pages has all of them.
+ *   q [B,Hq,d] dtype (BF16 or F16).  pages int32 [B,Hkv,n_sel]: logical pages, ascending, -1 behind the last.
+ * workspace: at least gdn_attn_select_workspace_size(B, Hkv, max_pages) bytes.
+ */
+size_t gdn_attn_select_workspace_size(int B, int Hkv, int max_pages);
+
+gdn_status_t gdn_attn_select(const void* q, const float* page_mean, const int32_t* page_table, const int32_t* lens,
+                             int B, int Hq, int Hkv, int d, int max_pages, int num_pages, int page_size, int n_sel,
+                             int n_first, int n_last, gdn_dtype_t dtype, int32_t* pages, void* workspace,
+                             size_t workspace_bytes, gdn_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,475 @@
+// attn_api.cuh -- the C ABI of the attention operators (declared in include/gdn.h): argument checks and
+// launches.  Included by gdn_lib.cu, whose error reporting it uses.
+#pragma once
+#include "attn_decode.cuh"
+#include "attn_page.cuh"
+#include "attn_prep.cuh"
+
+namespace {
+
+struct DeviceInfo {
+    int dev = -1, sms = 0;
+};
+
+// The current device and its SM count (looked up once per device).
+gdn_status_t device_info(DeviceInfo* out) {
+    static std::atomic<int> sms[64];
+    cudaError_t e = cudaGetDevice(&out->dev);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    int n = out->dev < 64 ? sms[out->dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, out->dev);
+        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "SM count: %s", cudaGetErrorString(e));
+        if (out->dev < 64) sms[out->dev].store(n, std::memory_order_relaxed);
+    }
+    out->sms = n;
+    return GDN_OK;
+}
+
+bool ranges_overlap(const void* a, long long na, const void* b, long long nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a != nullptr && b != nullptr && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+long long elem_size(int dt) { return dt == GDN_F32 ? 4 : 2; }
+
+// Bytes that `n` tokens of `width` elements, `stride` elements apart, span.
+long long span_bytes(long long n, long long stride, long long width, int dt) {
+    return n > 0 ? ((n - 1) * stride + width) * elem_size(dt) : 0;
+}
+
+#define REQUIRE_ATTN_HEADS()                                                                              \
+    do {                                                                                                  \
+        REQUIRE(Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0, "Hq=%d is not a positive multiple of Hkv=%d", Hq, Hkv); \
+        REQUIRE(Hq <= 65536, "Hq=%d too large", Hq);                                                      \
+    } while (0)
+
+#define REQUIRE_STRIDE(s, heads, name)                                                                  \
+    REQUIRE((s) >= (int64_t)(heads)*d && (s) % 8 == 0 && (s) < (1LL << 31),                               \
+            "%s=%lld: not a multiple of 8 of at least heads * d, below 2^31", name, (long long)(s))
+
+#define REQUIRE_PAGES()                                                                                     \
+    do {                                                                                                    \
+        REQUIRE(num_pages >= 1 && max_pages >= 1, "bad sizes num_pages=%d max_pages=%d", num_pages, max_pages); \
+        REQUIRE(page_size >= 1, "page_size=%d < 1", page_size);                                             \
+        if (page_size % 16 != 0 || page_size > 1024)                                                        \
+            return fail(GDN_ERR_UNSUPPORTED, "page_size=%d is not a multiple of 16 up to 1024", page_size); \
+        REQUIRE((long long)max_pages * page_size <= (1LL << 30), "max_pages * page_size above 2^30");       \
+    } while (0)
+
+// ---------------------------------------------------------------- norm and rotation
+
+// Heads per unit: the most (up to 8) that still give every SM about two blocks.
+int attn_heads_per_unit(long long rows, int lanes, int heads, int sms) {
+    int hps = 1;
+    while (hps < 8 && hps < heads && rows * lanes / (2 * hps) >= 2LL * sms * gdn::kAttnPrepThreads) hps *= 2;
+    return hps;
+}
+
+template <int IN, bool CACHE>
+gdn_status_t attn_prep_go(int d, const gdn::AttnPrepArgs& a, unsigned grid, cudaStream_t st) {
+    const char* name = CACHE ? "attn_prep_cache_kernel" : "attn_prep_kernel";
+    gdn::LaunchScope timed(st, name);
+    switch (d) {
+        case 16: gdn::attn_prep_kernel<IN, 16, CACHE><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        case 32: gdn::attn_prep_kernel<IN, 32, CACHE><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        case 64: gdn::attn_prep_kernel<IN, 64, CACHE><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        case 128: gdn::attn_prep_kernel<IN, 128, CACHE><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        default: gdn::attn_prep_kernel<IN, 256, CACHE><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+    }
+    return launched(name);
+}
+
+template <bool CACHE>
+gdn_status_t attn_prep_launch(gdn::AttnPrepArgs& a, int d, int in_dt, cudaStream_t st) {
+    DeviceInfo dev;
+    gdn_status_t r = device_info(&dev);
+    if (r != GDN_OK) return r;
+    const int lanes = d / 16;
+    a.hps = attn_heads_per_unit((long long)a.N * (a.Hq + (CACHE ? 2 : 1) * a.Hkv), lanes, a.Hq, dev.sms);
+    a.cq = (a.Hq + a.hps - 1) / a.hps;
+    a.ck = (a.Hkv + a.hps - 1) / a.hps;
+    const long long threads = (long long)a.N * (a.cq + (CACHE ? 2 : 1) * a.ck) * lanes;
+    const long long grid = (threads + gdn::kAttnPrepThreads - 1) / gdn::kAttnPrepThreads;
+    REQUIRE(grid * (gdn::kAttnPrepThreads / lanes) < (1LL << 31) && threads < (1LL << 32) - 256, "N=%d with Hq=%d too large",
+            a.N, a.Hq);
+    if (in_dt == GDN_F32) return attn_prep_go<gdn::kF32, CACHE>(d, a, (unsigned)grid, st);
+    if (in_dt == GDN_BF16) return attn_prep_go<gdn::kBF16, CACHE>(d, a, (unsigned)grid, st);
+    return attn_prep_go<gdn::kF16, CACHE>(d, a, (unsigned)grid, st);
+}
+
+template <int IN>
+gdn_status_t attn_prep_bwd_go(int d, const gdn::AttnPrepBwdArgs& a, unsigned grid, cudaStream_t st) {
+    gdn::LaunchScope timed(st, "attn_prep_bwd_kernel");
+    switch (d) {
+        case 16: gdn::attn_prep_bwd_kernel<IN, 16><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        case 32: gdn::attn_prep_bwd_kernel<IN, 32><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        case 64: gdn::attn_prep_bwd_kernel<IN, 64><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        case 128: gdn::attn_prep_bwd_kernel<IN, 128><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        default: gdn::attn_prep_bwd_kernel<IN, 256><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+    }
+    return launched("attn_prep_bwd_kernel");
+}
+
+constexpr int kAttnBwdBlocks = 2048;  // most blocks of the gradient kernel: sizes its workspace
+
+bool attn_head_dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128 || d == 256; }
+
+// ---------------------------------------------------------------- decode
+
+template <bool BF, int D, int NT, bool CHOSEN>
+gdn_status_t attn_decode_run(const gdn::AttnDecodeArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+    using S = gdn::AttnShape<D, NT>;
+    static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
+    static std::atomic<int> per_sm{0};
+    auto* kernel = gdn::attn_decode_kernel<BF, D, NT, CHOSEN>;
+    const unsigned long long bit = dev.dev < 64 ? 1ull << dev.dev : 0;
+    if ((ready.load(std::memory_order_acquire) & bit) == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        int n = 0;
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, gdn::kAttnThreads, S::SMEM);
+        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attn_decode_kernel: %s", cudaGetErrorString(e));
+        per_sm.store(n < 1 ? 1 : n, std::memory_order_relaxed);
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    int ctas = dev.sms * per_sm.load(std::memory_order_relaxed);
+    if (ctas > gdn::kAttnMaxCtas) ctas = gdn::kAttnMaxCtas;
+    {
+        gdn::LaunchScope timed(st, "attn_decode_kernel");
+        kernel<<<(unsigned)ctas, gdn::kAttnThreads, S::SMEM, st>>>(a);
+        gdn_status_t r = launched("attn_decode_kernel");
+        if (r != GDN_OK) return r;
+    }
+    // few work rows: many pieces each, so one head per block and eight warps over its pieces
+    const bool spread = (long long)a.B * a.Hkv * a.hblocks * 4 < ctas;
+    const int per = spread ? 1 : 8;
+    gdn::LaunchScope timed(st, "attn_join_kernel");
+    gdn::attn_join_kernel<D, NT><<<dim3((unsigned)ctas, (unsigned)(S::HB / per)), 256, 0, st>>>(a, ctas, per);
+    return launched("attn_join_kernel");
+}
+
+template <bool BF, int D>
+gdn_status_t attn_decode_d(const gdn::AttnDecodeArgs& a, int nt, const DeviceInfo& dev, cudaStream_t st) {
+    if constexpr (D < 256) {
+        if (nt == 2)
+            return a.pages == nullptr ? attn_decode_run<BF, D, 2, false>(a, dev, st)
+                                      : attn_decode_run<BF, D, 2, true>(a, dev, st);
+    }
+    return a.pages == nullptr ? attn_decode_run<BF, D, 1, false>(a, dev, st) : attn_decode_run<BF, D, 1, true>(a, dev, st);
+}
+
+template <bool BF>
+gdn_status_t attn_decode_bf(const gdn::AttnDecodeArgs& a, int d, int nt, const DeviceInfo& dev, cudaStream_t st) {
+    switch (d) {
+        case 32: return attn_decode_d<BF, 32>(a, nt, dev, st);
+        case 64: return attn_decode_d<BF, 64>(a, nt, dev, st);
+        case 128: return attn_decode_d<BF, 128>(a, nt, dev, st);
+        default: return attn_decode_d<BF, 256>(a, nt, dev, st);
+    }
+}
+
+bool attn_decode_dim_ok(int d) { return d == 32 || d == 64 || d == 128 || d == 256; }
+
+// Query-head tiles of 8 that a CTA takes together: two for groups above 8 (the keys are then read once for 16), but
+// one at d = 256, where two tiles' accumulators would spill (680 bytes a thread).
+int attn_head_tiles(int group, int d) { return group > 8 && d < 256 ? 2 : 1; }
+
+constexpr size_t kAttnMetaBytes = (size_t)gdn::kAttnMaxCtas * 2 * sizeof(int);
+
+template <bool BF>
+void attn_mean_launch(int d, const gdn::AttnMeanArgs& a, unsigned grid, cudaStream_t st) {
+    switch (d) {
+        case 32: gdn::attn_page_mean_kernel<BF, 32><<<grid, gdn::kMeanThreads, 0, st>>>(a); break;
+        case 64: gdn::attn_page_mean_kernel<BF, 64><<<grid, gdn::kMeanThreads, 0, st>>>(a); break;
+        case 128: gdn::attn_page_mean_kernel<BF, 128><<<grid, gdn::kMeanThreads, 0, st>>>(a); break;
+        default: gdn::attn_page_mean_kernel<BF, 256><<<grid, gdn::kMeanThreads, 0, st>>>(a); break;
+    }
+}
+
+template <bool BF>
+void attn_score_launch(int d, const gdn::AttnSelectArgs& a, unsigned grid, cudaStream_t st) {
+    switch (d) {
+        case 32: gdn::attn_score_kernel<BF, 32><<<grid, gdn::kScoreThreads, 0, st>>>(a); break;
+        case 64: gdn::attn_score_kernel<BF, 64><<<grid, gdn::kScoreThreads, 0, st>>>(a); break;
+        case 128: gdn::attn_score_kernel<BF, 128><<<grid, gdn::kScoreThreads, 0, st>>>(a); break;
+        default: gdn::attn_score_kernel<BF, 256><<<grid, gdn::kScoreThreads, 0, st>>>(a); break;
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status_t gdn_attn_prep(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const float* w_q,
+                           const float* w_k, float eps, const int32_t* positions, const double* inv_freq, int rot_dim,
+                           int N, int Hq, int Hkv, int d, gdn_dtype_t in_dtype, gdn_dtype_t out_dtype, void* q_out,
+                           void* k_out, gdn_stream_t stream) {
+    REQUIRE(N >= 0, "N=%d < 0", N);
+    REQUIRE_ATTN_HEADS();
+    REQUIRE(attn_head_dim_ok(d), "d=%d not in {16,32,64,128,256}", d);
+    REQUIRE(rot_dim >= 0 && rot_dim <= d && rot_dim % 16 == 0, "rot_dim=%d is not a multiple of 16 up to d", rot_dim);
+    REQUIRE(dtype_ok(in_dtype) && dtype_ok(out_dtype), "bad dtype");
+    REQUIRE(eps >= 0.f, "eps < 0");
+    REQUIRE_STRIDE(q_stride, Hq, "q_stride");
+    REQUIRE_STRIDE(k_stride, Hkv, "k_stride");
+    if (N == 0) return GDN_OK;
+    REQUIRE_PTR(q, "q"); REQUIRE_PTR(k, "k"); REQUIRE_PTR(w_q, "w_q"); REQUIRE_PTR(w_k, "w_k");
+    REQUIRE_PTR(positions, "positions"); REQUIRE_PTR(q_out, "q_out"); REQUIRE_PTR(k_out, "k_out");
+    if (rot_dim > 0) REQUIRE_PTR(inv_freq, "inv_freq");
+    const long long nq = (long long)N * Hq * d * elem_size(out_dtype), nk = (long long)N * Hkv * d * elem_size(out_dtype);
+    const long long sq = span_bytes(N, q_stride, (long long)Hq * d, in_dtype);
+    const long long sk = span_bytes(N, k_stride, (long long)Hkv * d, in_dtype);
+    const bool q_in_place = q_out == q && q_stride == (int64_t)Hq * d && in_dtype == out_dtype;
+    const bool k_in_place = k_out == k && k_stride == (int64_t)Hkv * d && in_dtype == out_dtype;
+    REQUIRE(!ranges_overlap(q_out, nq, k_out, nk), "q_out overlaps k_out");
+    REQUIRE((q_in_place || !ranges_overlap(q_out, nq, q, sq)) && !ranges_overlap(q_out, nq, k, sk) &&
+                (k_in_place || !ranges_overlap(k_out, nk, k, sk)) && !ranges_overlap(k_out, nk, q, sq),
+            "an output overlaps an input");
+    gdn::AttnPrepArgs a{};
+    a.q = q; a.k = k; a.v = nullptr; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = 0;
+    a.w_q = w_q; a.w_k = w_k; a.eps = eps; a.positions = positions; a.inv_freq = inv_freq; a.rot = rot_dim;
+    a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.out_dt = (int)out_dtype; a.q_out = q_out; a.k_out = k_out;
+    return attn_prep_launch<false>(a, d, (int)in_dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gdn_status_t gdn_attn_prep_cache(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                 int64_t v_stride, const float* w_q, const float* w_k, float eps,
+                                 const int32_t* positions, const double* inv_freq, int rot_dim,
+                                 const int32_t* cu_seqlens, int num_seqs, int N, int Hq, int Hkv, int d,
+                                 const int32_t* page_table, int max_pages, int num_pages, int page_size,
+                                 gdn_dtype_t in_dtype, gdn_dtype_t out_dtype, void* q_out, void* k_cache, void* v_cache,
+                                 gdn_stream_t stream) {
+    REQUIRE(N >= 0 && num_seqs >= 1, "bad sizes N=%d num_seqs=%d", N, num_seqs);
+    REQUIRE_ATTN_HEADS();
+    REQUIRE(attn_head_dim_ok(d), "d=%d not in {16,32,64,128,256}", d);
+    REQUIRE(rot_dim >= 0 && rot_dim <= d && rot_dim % 16 == 0, "rot_dim=%d is not a multiple of 16 up to d", rot_dim);
+    REQUIRE(dtype_ok(in_dtype) && dtype_ok(out_dtype), "bad dtype");
+    REQUIRE(eps >= 0.f, "eps < 0");
+    REQUIRE_STRIDE(q_stride, Hq, "q_stride");
+    REQUIRE_STRIDE(k_stride, Hkv, "k_stride");
+    REQUIRE_STRIDE(v_stride, Hkv, "v_stride");
+    REQUIRE(cu_seqlens != nullptr || N % num_seqs == 0, "N=%d not a multiple of num_seqs=%d", N, num_seqs);
+    REQUIRE_PAGES();
+    if (out_dtype == GDN_F32)
+        return fail(GDN_ERR_UNSUPPORTED, "gdn_attn_prep_cache is built for 16-bit caches");
+    if (N == 0) return GDN_OK;
+    REQUIRE_PTR(q, "q"); REQUIRE_PTR(k, "k"); REQUIRE_PTR(v, "v"); REQUIRE_PTR(w_q, "w_q"); REQUIRE_PTR(w_k, "w_k");
+    REQUIRE_PTR(positions, "positions"); REQUIRE_PTR(page_table, "page_table"); REQUIRE_PTR(q_out, "q_out");
+    REQUIRE_PTR(k_cache, "k_cache"); REQUIRE_PTR(v_cache, "v_cache"); OPT_PTR(cu_seqlens, "cu_seqlens");
+    if (rot_dim > 0) REQUIRE_PTR(inv_freq, "inv_freq");
+    const long long nq = (long long)N * Hq * d * 2, nc = (long long)num_pages * Hkv * page_size * d * 2;
+    const long long sq = span_bytes(N, q_stride, (long long)Hq * d, in_dtype);
+    const long long sk = span_bytes(N, k_stride, (long long)Hkv * d, in_dtype);
+    const long long sv = span_bytes(N, v_stride, (long long)Hkv * d, in_dtype);
+    const bool in_place = q_out == q && q_stride == (int64_t)Hq * d && in_dtype == out_dtype;
+    REQUIRE((in_place || !ranges_overlap(q_out, nq, q, sq)) && !ranges_overlap(q_out, nq, k, sk) &&
+                !ranges_overlap(q_out, nq, v, sv),
+            "q_out overlaps an input");
+    const void* caches[2] = {k_cache, v_cache};
+    for (const void* c : caches)
+        REQUIRE(!ranges_overlap(c, nc, q, sq) && !ranges_overlap(c, nc, k, sk) && !ranges_overlap(c, nc, v, sv) &&
+                    !ranges_overlap(c, nc, q_out, nq),
+                "a cache overlaps another tensor");
+    REQUIRE(!ranges_overlap(k_cache, nc, v_cache, nc), "k_cache overlaps v_cache");
+    gdn::AttnPrepArgs a{};
+    a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.w_q = w_q; a.w_k = w_k; a.eps = eps; a.positions = positions; a.inv_freq = inv_freq; a.rot = rot_dim;
+    a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.out_dt = (int)out_dtype; a.q_out = q_out; a.k_out = k_cache; a.v_out = v_cache;
+    a.cu = cu_seqlens; a.table = page_table; a.num_seqs = num_seqs; a.max_pages = max_pages; a.num_pages = num_pages;
+    a.page_size = page_size;
+    return attn_prep_launch<true>(a, d, (int)in_dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_attn_prep_bwd_workspace_size(int d) {
+    return attn_head_dim_ok(d) ? (size_t)kAttnBwdBlocks * d * sizeof(float) : 0;
+}
+
+gdn_status_t gdn_attn_prep_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, int64_t q_stride,
+                               int64_t k_stride, const float* w_q, const float* w_k, float eps,
+                               const int32_t* positions, const double* inv_freq, int rot_dim, int N, int Hq, int Hkv,
+                               int d, gdn_dtype_t in_dtype, gdn_dtype_t dy_dtype, void* dq, void* dk, float* dw_q,
+                               float* dw_k, void* workspace, size_t workspace_bytes, gdn_stream_t stream) {
+    REQUIRE(N >= 0, "N=%d < 0", N);
+    REQUIRE_ATTN_HEADS();
+    REQUIRE(attn_head_dim_ok(d), "d=%d not in {16,32,64,128,256}", d);
+    REQUIRE(rot_dim >= 0 && rot_dim <= d && rot_dim % 16 == 0, "rot_dim=%d is not a multiple of 16 up to d", rot_dim);
+    REQUIRE(dtype_ok(in_dtype) && dtype_ok(dy_dtype), "bad dtype");
+    REQUIRE(eps >= 0.f, "eps < 0");
+    REQUIRE_STRIDE(q_stride, Hq, "q_stride");
+    REQUIRE_STRIDE(k_stride, Hkv, "k_stride");
+    REQUIRE_PTR(dw_q, "dw_q"); REQUIRE_PTR(dw_k, "dw_k");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (N == 0) {  // no token: zero gradients of the weights
+        cudaError_t e = cudaMemsetAsync(dw_q, 0, (size_t)d * 4, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dw_k, 0, (size_t)d * 4, st);
+        return e == cudaSuccess ? GDN_OK : fail(GDN_ERR_CUDA, "memset: %s", cudaGetErrorString(e));
+    }
+    REQUIRE_PTR(dq_out, "dq_out"); REQUIRE_PTR(dk_out, "dk_out"); REQUIRE_PTR(q, "q"); REQUIRE_PTR(k, "k");
+    REQUIRE_PTR(w_q, "w_q"); REQUIRE_PTR(w_k, "w_k"); REQUIRE_PTR(positions, "positions");
+    REQUIRE_PTR(dq, "dq"); REQUIRE_PTR(dk, "dk"); REQUIRE_PTR(workspace, "workspace");
+    if (rot_dim > 0) REQUIRE_PTR(inv_freq, "inv_freq");
+    REQUIRE(workspace_bytes >= gdn_attn_prep_bwd_workspace_size(d), "workspace of %zu bytes, %zu needed", workspace_bytes,
+            gdn_attn_prep_bwd_workspace_size(d));
+    const long long oq = (long long)N * Hq * d * elem_size(in_dtype), ok = (long long)N * Hkv * d * elem_size(in_dtype);
+    const long long gq = (long long)N * Hq * d * elem_size(dy_dtype), gk = (long long)N * Hkv * d * elem_size(dy_dtype);
+    const long long sq = span_bytes(N, q_stride, (long long)Hq * d, in_dtype);
+    const long long sk = span_bytes(N, k_stride, (long long)Hkv * d, in_dtype);
+    const void* outs[2] = {dq, dk};
+    for (int i = 0; i < 2; ++i) {
+        const long long n = i == 0 ? oq : ok;
+        REQUIRE(!ranges_overlap(outs[i], n, dq_out, gq) && !ranges_overlap(outs[i], n, dk_out, gk) &&
+                    !ranges_overlap(outs[i], n, q, sq) && !ranges_overlap(outs[i], n, k, sk),
+                "an output overlaps an input");
+    }
+    REQUIRE(!ranges_overlap(dq, oq, dk, ok), "dq overlaps dk");
+    DeviceInfo dev;
+    gdn_status_t r = device_info(&dev);
+    if (r != GDN_OK) return r;
+    const int lanes = d / 16, subs = gdn::kAttnPrepThreads / lanes;
+    gdn::AttnPrepBwdArgs a{};
+    a.q = q; a.k = k; a.dyq = dq_out; a.dyk = dk_out; a.q_stride = q_stride; a.k_stride = k_stride;
+    a.w_q = w_q; a.w_k = w_k; a.eps = eps; a.positions = positions; a.inv_freq = inv_freq; a.rot = rot_dim;
+    a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.dy_dt = (int)dy_dtype; a.dq = dq; a.dk = dk;
+    a.partial = reinterpret_cast<float*>(workspace);
+    a.hps = attn_heads_per_unit((long long)N * (Hq + Hkv), lanes, Hq, dev.sms);
+    a.cq = (Hq + a.hps - 1) / a.hps;
+    a.ck = (Hkv + a.hps - 1) / a.hps;
+    const long long uq = (long long)N * a.cq, uk = (long long)N * a.ck;
+    REQUIRE(uq < (1LL << 30) && uk < (1LL << 30), "N=%d with Hq=%d too large", N, Hq);
+    // resident blocks, shared out between queries and keys by their rows
+    const long long want = 2LL * dev.sms < kAttnBwdBlocks ? 2LL * dev.sms : kAttnBwdBlocks;
+    long long bq = want * Hq / (Hq + Hkv), bk = want - bq;
+    bq = bq < 1 ? 1 : bq;
+    bk = bk < 1 ? 1 : bk;
+    if (bq > (uq + subs - 1) / subs) bq = (uq + subs - 1) / subs;
+    if (bk > (uk + subs - 1) / subs) bk = (uk + subs - 1) / subs;
+    a.gq = (int)bq;
+    const unsigned blocks = (unsigned)(bq + bk);
+    if (in_dtype == GDN_F32) r = attn_prep_bwd_go<gdn::kF32>(d, a, blocks, st);
+    else if (in_dtype == GDN_BF16) r = attn_prep_bwd_go<gdn::kBF16>(d, a, blocks, st);
+    else r = attn_prep_bwd_go<gdn::kF16>(d, a, blocks, st);
+    if (r != GDN_OK) return r;
+    gdn::LaunchScope timed(st, "attn_prep_dw_kernel");
+    gdn::attn_prep_dw_kernel<<<dim3(2, (unsigned)((d + 31) / 32)), dim3(32, 8), 0, st>>>(a.partial, a.gq, (int)blocks, d,
+                                                                                         dw_q, dw_k);
+    return launched("attn_prep_dw_kernel");
+}
+
+size_t gdn_attn_decode_workspace_size(int Hq, int Hkv, int d) {
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !attn_decode_dim_ok(d)) return 0;
+    const int nt = attn_head_tiles(Hq / Hkv, d);
+    return kAttnMetaBytes + (size_t)gdn::kAttnMaxCtas * 2 * 8 * nt * (d + 2) * sizeof(float);
+}
+
+gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                             const int32_t* lens, const int32_t* pages, int n_sel, int B, int Hq, int Hkv, int d,
+                             int max_pages, int num_pages, int page_size, float scale, gdn_dtype_t dtype,
+                             gdn_dtype_t y_dtype, void* y, void* workspace, size_t workspace_bytes, gdn_stream_t stream) {
+    REQUIRE(B >= 0, "B=%d < 0", B);
+    REQUIRE_ATTN_HEADS();
+    REQUIRE(d >= 1, "d=%d < 1", d);
+    REQUIRE(dtype_ok(dtype) && dtype_ok(y_dtype), "bad dtype");
+    REQUIRE(scale == scale, "scale is NaN");
+    if (!attn_decode_dim_ok(d) || dtype == GDN_F32)
+        return fail(GDN_ERR_UNSUPPORTED, "gdn_attn_decode is built for d in {32,64,128,256} and 16-bit caches (d=%d)", d);
+    REQUIRE_PAGES();
+    if (pages != nullptr)
+        REQUIRE(n_sel >= 1 && (long long)n_sel * page_size <= (1LL << 30), "bad n_sel=%d", n_sel);
+    REQUIRE((long long)B * Hq < (1LL << 31), "B * Hq too large");
+    if (B == 0) return GDN_OK;
+    REQUIRE_PTR(q, "q"); REQUIRE_PTR(k_cache, "k_cache"); REQUIRE_PTR(v_cache, "v_cache");
+    REQUIRE_PTR(page_table, "page_table"); REQUIRE_PTR(lens, "lens"); REQUIRE_PTR(y, "y"); OPT_PTR(pages, "pages");
+    REQUIRE_PTR(workspace, "workspace");
+    REQUIRE(workspace_bytes >= gdn_attn_decode_workspace_size(Hq, Hkv, d), "workspace of %zu bytes, %zu needed",
+            workspace_bytes, gdn_attn_decode_workspace_size(Hq, Hkv, d));
+    REQUIRE(!ranges_overlap(y, (long long)B * Hq * d * elem_size(y_dtype), q, (long long)B * Hq * d * 2), "y overlaps q");
+    DeviceInfo dev;
+    gdn_status_t r = device_info(&dev);
+    if (r != GDN_OK) return r;
+    gdn::AttnDecodeArgs a{};
+    const int nt = attn_head_tiles(Hq / Hkv, d);
+    a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.table = page_table; a.lens = lens; a.pages = pages;
+    a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.group = Hq / Hkv; a.hblocks = (a.group + 8 * nt - 1) / (8 * nt);
+    a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages; a.n_sel = pages != nullptr ? n_sel : 0;
+    a.tiles_per_page = page_size / 16;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.y_dt = (int)y_dtype;
+    a.y = y;
+    a.meta = reinterpret_cast<int*>(workspace);
+    a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kAttnMetaBytes);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == GDN_BF16 ? attn_decode_bf<true>(a, d, nt, dev, st) : attn_decode_bf<false>(a, d, nt, dev, st);
+}
+
+gdn_status_t gdn_attn_page_mean(const void* k_cache, const int32_t* page_table, const int32_t* lens,
+                                const int32_t* starts, int B, int Hkv, int d, int max_pages, int num_pages,
+                                int page_size, gdn_dtype_t dtype, float* page_mean, gdn_stream_t stream) {
+    REQUIRE(B >= 0 && Hkv >= 1 && Hkv <= 65536, "bad sizes B=%d Hkv=%d", B, Hkv);
+    REQUIRE(d >= 1 && dtype_ok(dtype), "bad d=%d or dtype", d);
+    if (!attn_decode_dim_ok(d) || dtype == GDN_F32)
+        return fail(GDN_ERR_UNSUPPORTED, "gdn_attn_page_mean is built for d in {32,64,128,256} and 16-bit caches (d=%d)", d);
+    REQUIRE_PAGES();
+    if (B == 0) return GDN_OK;
+    REQUIRE_PTR(k_cache, "k_cache"); REQUIRE_PTR(page_table, "page_table"); REQUIRE_PTR(lens, "lens");
+    REQUIRE_PTR(page_mean, "page_mean"); OPT_PTR(starts, "starts");
+    DeviceInfo dev;
+    gdn_status_t r = device_info(&dev);
+    if (r != GDN_OK) return r;
+    gdn::AttnMeanArgs a{};
+    a.k_cache = k_cache; a.table = page_table; a.lens = lens; a.starts = starts; a.B = B; a.Hkv = Hkv;
+    a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages; a.mean = page_mean;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const long long most = (long long)B * Hkv * max_pages;  // units at most
+    const unsigned grid = (unsigned)(most < 8LL * dev.sms ? most : 8LL * dev.sms);
+    gdn::LaunchScope timed(st, "attn_page_mean_kernel");
+    if (dtype == GDN_BF16) attn_mean_launch<true>(d, a, grid, st);
+    else attn_mean_launch<false>(d, a, grid, st);
+    return launched("attn_page_mean_kernel");
+}
+
+size_t gdn_attn_select_workspace_size(int B, int Hkv, int max_pages) {
+    return B < 1 || Hkv < 1 || max_pages < 1 ? 0 : (size_t)B * Hkv * max_pages * sizeof(unsigned long long);
+}
+
+gdn_status_t gdn_attn_select(const void* q, const float* page_mean, const int32_t* page_table, const int32_t* lens,
+                             int B, int Hq, int Hkv, int d, int max_pages, int num_pages, int page_size, int n_sel,
+                             int n_first, int n_last, gdn_dtype_t dtype, int32_t* pages, void* workspace,
+                             size_t workspace_bytes, gdn_stream_t stream) {
+    REQUIRE(B >= 0, "B=%d < 0", B);
+    REQUIRE_ATTN_HEADS();
+    REQUIRE(d >= 1 && dtype_ok(dtype), "bad d=%d or dtype", d);
+    if (!attn_decode_dim_ok(d) || dtype == GDN_F32)
+        return fail(GDN_ERR_UNSUPPORTED, "gdn_attn_select is built for d in {32,64,128,256} and 16-bit queries (d=%d)", d);
+    REQUIRE_PAGES();
+    REQUIRE(n_sel >= 1 && (long long)n_sel * page_size <= (1LL << 30), "bad n_sel=%d", n_sel);
+    REQUIRE(n_first >= 0 && n_last >= 0 && (long long)n_first + n_last <= n_sel, "n_first=%d, n_last=%d: not within n_sel=%d",
+            n_first, n_last, n_sel);
+    REQUIRE((long long)B * Hkv <= 0x7fffffffLL, "B * Hkv too large");
+    if (B == 0) return GDN_OK;
+    REQUIRE_PTR(q, "q"); REQUIRE_PTR(page_mean, "page_mean"); REQUIRE_PTR(page_table, "page_table");
+    REQUIRE_PTR(lens, "lens"); REQUIRE_PTR(pages, "pages"); REQUIRE_PTR(workspace, "workspace");
+    REQUIRE(workspace_bytes >= gdn_attn_select_workspace_size(B, Hkv, max_pages), "workspace of %zu bytes, %zu needed",
+            workspace_bytes, gdn_attn_select_workspace_size(B, Hkv, max_pages));
+    DeviceInfo dev;
+    gdn_status_t r = device_info(&dev);
+    if (r != GDN_OK) return r;
+    gdn::AttnSelectArgs a{};
+    a.q = q; a.mean = page_mean; a.table = page_table; a.lens = lens; a.B = B; a.Hq = Hq; a.Hkv = Hkv;
+    a.group = Hq / Hkv; a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages; a.n_sel = n_sel;
+    a.n_first = n_first; a.n_last = n_last; a.keys = reinterpret_cast<unsigned long long*>(workspace); a.pages = pages;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (max_pages > n_sel) {  // else every row has all its pages chosen
+        const long long most = (long long)B * Hkv * ((max_pages + gdn::kScorePages - 1) / gdn::kScorePages);
+        const unsigned grid = (unsigned)(most < 4LL * dev.sms ? most : 4LL * dev.sms);
+        gdn::LaunchScope timed(st, "attn_score_kernel");
+        if (dtype == GDN_BF16) attn_score_launch<true>(d, a, grid, st);
+        else attn_score_launch<false>(d, a, grid, st);
+        r = launched("attn_score_kernel");
+        if (r != GDN_OK) return r;
+    }
+    gdn::LaunchScope timed(st, "attn_select_kernel");
+    gdn::attn_select_kernel<<<(unsigned)((long long)B * Hkv), gdn::kSelectThreads, 0, st>>>(a);
+    return launched("attn_select_kernel");
+}
+
+}  // extern "C"

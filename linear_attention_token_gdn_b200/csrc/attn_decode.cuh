@@ -1,0 +1,514 @@
+// attn_decode.cuh -- softmax attention of one new token per row over a paged key-value cache, the
+// serving step of the attention layer between GDN mixers, over all of a row's keys or over chosen pages.
+//
+// Per (row, query head), over the row's keys j (key head = query head / group):
+//   s_j = scale q . k_j,   y = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),   m = max_j s_j.
+// One pass with a running m, l = sum e^(s - m) and o = sum e^(s - m) v, all fp32.
+//
+// Bound by HBM: every key and value is read once (4 flop per 2-byte element and query head of the group).
+//
+// Split.  The rows' lengths live on the device, so the grid is fixed (every CTA resident) and the
+// work is cut on the device: the tiles of 16 keys of all (row, key head) pairs stand in one line, and
+// each CTA takes an equal stretch of it.  A stretch holds whole pairs, whose results are final, and at
+// most two pieces of pairs that neighbours share: o, m and l of those go to the workspace, and a second
+// small kernel joins them in the order of the line, so results do not depend on timing.
+//
+// Tile.  A warp takes 16 keys at a time, S^T = K Q^T and O^T = V^T P^T by mma.sync m16n8k16: the group's
+// query heads are the 8 columns (16 in two tiles), so a group of 8 wastes nothing, and no operand goes
+// through shared memory.  The contraction runs over channels in any order, so a lane's part of K, 4
+// channels out of 16, is 8 adjacent channels for two steps: a 16-byte load gives both.  The same for V
+// with two keys' words interleaved by byte permutes (the fragment wants adjacent keys of one channel).
+// P goes from the accumulators to the B operand by movmatrix.  The K registers are refilled as soon as
+// S is formed, the V registers as soon as O is updated, so a warp always has 4 to 8 KB (d = 128) in flight.
+// P enters as a 16-bit value and its 16-bit remainder: a single rounding (2^-9 for bf16) would add as much
+// error as the output's own rounding, and the tensor pipe has the room.
+// m follows the scores lazily: it moves only when a score exceeds it by more than 8 (in log2), so p is at
+// most 2^8, and most tiles need one vote instead of a reduction over lanes and a rescale.
+#pragma once
+#include "attn_prep.cuh"
+#include "common.cuh"
+#include "warp_mma.cuh"
+
+namespace gdn {
+
+constexpr int kAttnWarps = 4, kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnMaxCtas = 640;  // grid bound: sizes the workspace
+constexpr int kAttnMinTiles = 4;   // least tiles per CTA: one per warp
+
+// A place in the line of all rows' work items: row `b`, whose items start at `before`; `total` of all rows.
+struct AttnPlace {
+    int b;
+    long long before, total;
+};
+
+__device__ __forceinline__ long long warp_scan(long long x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((int)(threadIdx.x & 31) >= o) x += y;
+    }
+    return x;
+}
+
+// Finds the row of item `target(total)` in the line of count(b) items for b < B; all threads of the CTA call
+// it and get the same answer.  b = B when the target is not below the total.
+template <int THREADS, class Count, class Target>
+__device__ __forceinline__ AttnPlace attn_locate(int B, Count count, Target target) {
+    __shared__ long long s_warp[THREADS / 32];
+    __shared__ long long s_before;
+    __shared__ int s_b;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long total = 0;
+    for (int b = threadIdx.x; b < B; b += THREADS) total += count(b);
+    long long first = total;  // this thread's row of the first (often only) chunk, when B <= THREADS
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) s_warp[warp] = total;
+    if (threadIdx.x == 0) s_b = B;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) total += s_warp[w];
+    const long long want = target(total);
+    long long carry = 0;
+    if (want < total) {
+        for (int base = 0; base < B; base += THREADS) {
+            const int b = base + threadIdx.x;
+            const long long n = B <= THREADS ? first : (b < B ? count(b) : 0);
+            long long incl = warp_scan(n);
+            __syncthreads();  // s_warp read by everyone
+            if (lane == 31) s_warp[warp] = incl;
+            __syncthreads();
+            incl += carry;
+#pragma unroll
+            for (int w = 0; w < THREADS / 32; ++w) {
+                if (w < warp) incl += s_warp[w];
+                carry += s_warp[w];
+            }
+            if (b < B && want < incl && want >= incl - n) {
+                s_b = b;
+                s_before = incl - n;
+            }
+            if (carry > want) break;  // uniform: carry is the same in all threads
+        }
+    }
+    __syncthreads();
+    AttnPlace p;
+    p.b = s_b;
+    p.before = s_b < B ? s_before : total;
+    p.total = total;
+    return p;
+}
+
+// Length of row b, bounded (and flagged) to what its page table can hold.
+__device__ __forceinline__ int attn_len(const int32_t* lens, int b, long long capacity) {
+    const int n = lens[b];
+    if (n < 0 || n > capacity) {
+        raise_error(kErrPage);
+        return n < 0 ? 0 : (int)capacity;
+    }
+    return n;
+}
+
+struct AttnDecodeArgs {
+    const void *q, *k_cache, *v_cache;
+    const int32_t *table, *lens, *pages;        // pages: [B, Hkv, n_sel] logical pages, or NULL (all)
+    int B, Hq, Hkv, group, hblocks;             // hblocks: blocks of 8 NT heads per group
+    int num_pages, page_size, max_pages, n_sel, tiles_per_page;
+    float scale_log2;                           // scale * log2(e)
+    int y_dt;
+    void* y;
+    int* meta;                                  // [grid][2]: row of the starting piece (-1: none); continuing piece:
+                                                // 0 none, 1 goes on, 2 ends
+    float* part;                                // [grid][2][8 NT][D + 2]: o, then m and l (log2 scale)
+};
+
+// The tiles of row b for one of its (key head, head block) pairs.
+__device__ __forceinline__ int attn_tiles(const AttnDecodeArgs& a, int b, int len) {
+    return a.pages == nullptr ? (len + 15) >> 4 : len > 0 ? a.n_sel * a.tiles_per_page : 0;
+}
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// (x0, x1) -> 16-bit pairs hi = round(x), lo = round(x - hi)
+template <bool BF>
+__device__ __forceinline__ void split16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    hi = pack2<BF>(x0, x1);
+    const float2 f = unpack2<BF>(hi);
+    lo = pack2<BF>(x0 - f.x, x1 - f.y);
+}
+
+// 4 or 2 words of a cache row, read once: no line of it is kept in L1.
+template <int W>
+__device__ __forceinline__ void ld_stream(const void* p, uint32_t* r) {
+    if constexpr (W == 4)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "l"(p));
+    else
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+}
+
+template <int D, int NT>
+struct AttnShape {
+    static constexpr int KC = D / 32;                    // 16-byte loads of a key per lane
+    static constexpr int VW = D >= 64 ? 4 : 2;           // words of a value load
+    static constexpr int VC = D / (16 * VW);             // loads of a value per lane
+    static constexpr int MT = D / 16;                    // 16-channel tiles of O^T
+    static constexpr int HB = 8 * NT;                    // heads of a block
+    static constexpr int PIECE = HB * (D + 2);           // floats of a piece: o, m, l
+    // p is formed 2^7 larger for fp16, at most 2^15: small weights then keep 7 more bits above fp16's smallest step.
+    // l carries the same factor, so it drops out.
+    __host__ __device__ static constexpr float kLift(bool bf) { return bf ? 0.0f : 7.0f; }
+    static constexpr int SMEM = (kAttnWarps * HB * D + 2 * kAttnWarps * HB) * 4;
+};
+
+template <bool BF, int D, int NT, bool CHOSEN>
+__global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDecodeArgs a) {
+    using S = AttnShape<D, NT>;
+    extern __shared__ __align__(16) float s_o[];         // [warp][head][D], then m and l [warp][head]
+    float* const s_m = s_o + kAttnWarps * S::HB * D;
+    float* const s_l = s_m + kAttnWarps * S::HB;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int pairs = a.Hkv * a.hblocks;                 // work rows of a row
+    const long long capacity = (long long)a.max_pages * a.page_size;
+    const int cta = blockIdx.x;
+
+    // rows without a key
+    for (int b = cta; b < a.B; b += gridDim.x) {
+        if (a.lens[b] <= 0)
+            for (int i = tid; i < a.Hq * D; i += kAttnThreads) st1(a.y, a.y_dt, (size_t)b * a.Hq * D + i, 0.0f);
+    }
+
+    long long share = 0;
+    AttnPlace place = attn_locate<kAttnThreads>(
+        a.B, [&](int b) { return (long long)attn_tiles(a, b, attn_len(a.lens, b, capacity)) * pairs; },
+        [&](long long total) {
+            share = (total + gridDim.x - 1) / gridDim.x;
+            share = (share + kAttnMinTiles - 1) / kAttnMinTiles * kAttnMinTiles;
+            return share * cta;
+        });
+    long long at = share * cta;
+    const long long end = at + share < place.total ? at + share : place.total;
+    int starting = -1, continuing = 0;
+
+    int b = place.b;
+    long long row_base = place.before;                   // the line's index of b's first tile
+    while (at < end) {                                   // one (row, key head, head block) piece per turn
+        int len = attn_len(a.lens, b, capacity);
+        int tiles = attn_tiles(a, b, len);
+        while (at >= row_base + (long long)tiles * pairs) {
+            row_base += (long long)tiles * pairs;
+            ++b;
+            len = attn_len(a.lens, b, capacity);
+            tiles = attn_tiles(a, b, len);
+        }
+        const int pair = (int)((at - row_base) / tiles);
+        const int hk = pair / a.hblocks, hb = pair - hk * a.hblocks;
+        const int first = (int)(at - row_base - (long long)pair * tiles);
+        const int last = (int)(end - at < tiles - first ? first + (end - at) : tiles);  // tiles [first, last)
+        const int h0 = hk * a.group + hb * S::HB;
+        const int heads = min(S::HB, a.group - hb * S::HB);
+        const int32_t* table = a.table + (size_t)b * a.max_pages;
+        const int32_t* list = CHOSEN ? a.pages + ((size_t)b * a.Hkv + hk) * a.n_sel : nullptr;
+        const int pages = (len + a.page_size - 1) / a.page_size;
+
+        // Q as the B operand: lane (g, t) holds channels 32 c + 8 t ... + 7 of head g
+        uint32_t qf[NT][S::KC][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int h = 8 * n + g;
+#pragma unroll
+            for (int c = 0; c < S::KC; ++c) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (h < heads)
+                    x = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
+                                                        ((size_t)b * a.Hq + h0 + h) * D + 32 * c + 8 * t);
+                qf[n][c][0] = x.x; qf[n][c][1] = x.y; qf[n][c][2] = x.z; qf[n][c][3] = x.w;
+            }
+        }
+
+        float o[NT][S::MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < S::MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
+        }
+
+        // A tile's place: keys of the tile inside the row (0: nothing to do), and the element of its first key.
+        auto find = [&](int tile, size_t& base) -> int {
+            int page = tile / a.tiles_per_page;
+            const int off = (tile - page * a.tiles_per_page) * 16;
+            if (CHOSEN) {
+                page = list[page];
+                if (page < 0) return 0;                  // padding of the list
+                if (page >= pages) {
+                    if (lane == 0) raise_error(kErrPage);
+                    return 0;
+                }
+            }
+            const int left = len - (page * a.page_size + off);
+            if (left <= 0) return 0;
+            const int phys = table[page];
+            if (phys < 0 || phys >= a.num_pages) {
+                if (lane == 0) raise_error(kErrPage);
+                return 0;
+            }
+            base = (((size_t)phys * a.Hkv + hk) * a.page_size + off) * D;
+            if (!in_bounds((long long)base + 16 * D - 1, (long long)a.num_pages * a.Hkv * a.page_size * D)) return 0;
+            return left < 16 ? left : 16;
+        };
+        // Keys behind the row's last one are never read: their lanes read the tile's first key instead.
+        uint32_t kf[2][S::KC][4], vf[4][S::VC][S::VW];
+        auto load_k = [&](size_t base, int n) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int key = g + 8 * i < n ? g + 8 * i : 0;
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(a.k_cache) + base + key * D + 8 * t;
+#pragma unroll
+                for (int c = 0; c < S::KC; ++c) ld_stream<4>(p + 32 * c, kf[i][c]);
+            }
+        };
+        auto load_v = [&](size_t base, int n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at_key = 2 * t + (i & 1) + 8 * (i >> 1);
+                const int key = at_key < n ? at_key : 0;
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(a.v_cache) + base + key * D + 2 * S::VW * g;
+#pragma unroll
+                for (int c = 0; c < S::VC; ++c) ld_stream<S::VW>(p + 16 * S::VW * c, vf[i][c]);
+            }
+        };
+
+        int tile = first + warp;
+        size_t base = 0;
+        int n_keys = 0;
+        auto advance = [&]() {  // the warp's next tile with a key in it
+            n_keys = 0;
+            while (tile < last && (n_keys = find(tile, base)) == 0) tile += kAttnWarps;
+        };
+        advance();
+        if (n_keys > 0) {
+            load_k(base, n_keys);
+            load_v(base, n_keys);
+        }
+        while (n_keys > 0) {
+            const int n_now = n_keys;
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < S::KC; ++c) {
+                    const uint32_t lo[4] = {kf[0][c][0], kf[1][c][0], kf[0][c][1], kf[1][c][1]};
+                    const uint32_t hi[4] = {kf[0][c][2], kf[1][c][2], kf[0][c][3], kf[1][c][3]};
+                    wm::mma16816x<BF>(s[n], lo, qf[n][c][0], qf[n][c][1]);
+                    wm::mma16816x<BF>(s[n], hi, qf[n][c][2], qf[n][c][3]);
+                }
+            }
+            tile += kAttnWarps;
+            advance();
+            if (n_keys > 0) load_k(base, n_keys);
+
+            // lane (g, t): keys g (0, 1) and g + 8 (2, 3) of heads 2 t and 2 t + 1
+            bool grow = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[n][e] *= a.scale_log2;
+                    if (g + 8 * (e >> 1) >= n_now) s[n][e] = -INFINITY;
+                    grow |= s[n][e] > m[n][e & 1] + 8.0f;
+                }
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(m[n][e], fmaxf(s[n][e], s[n][e + 2]));
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                        const float f = top == -INFINITY ? 1.0f : exp2f(m[n][e] - top);
+                        m[n][e] = top;
+                        l[n][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < S::MT; ++i) {
+                            o[n][i][e] *= f;
+                            o[n][i][e + 2] *= f;
+                        }
+                    }
+                }
+            }
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float m0 = (m[n][0] == -INFINITY ? 0.0f : m[n][0]) - S::kLift(BF);
+                const float m1 = (m[n][1] == -INFINITY ? 0.0f : m[n][1]) - S::kLift(BF);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float p0 = exp2f(s[n][2 * i] - m0), p1 = exp2f(s[n][2 * i + 1] - m1);
+                    l[n][0] += p0;
+                    l[n][1] += p1;
+                    uint32_t hi, lo;
+                    split16<BF>(p0, p1, hi, lo);
+                    ph[n][i] = movmatrix(hi);
+                    pl[n][i] = movmatrix(lo);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < S::VC; ++c) {
+#pragma unroll
+                for (int w = 0; w < S::VW; ++w) {
+                    const uint32_t vt[4] = {__byte_perm(vf[0][c][w], vf[1][c][w], 0x5410),
+                                            __byte_perm(vf[0][c][w], vf[1][c][w], 0x7632),
+                                            __byte_perm(vf[2][c][w], vf[3][c][w], 0x5410),
+                                            __byte_perm(vf[2][c][w], vf[3][c][w], 0x7632)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        wm::mma16816x<BF>(o[n][c * S::VW + w], vt, pl[n][0], pl[n][1]);
+                        wm::mma16816x<BF>(o[n][c * S::VW + w], vt, ph[n][0], ph[n][1]);
+                    }
+                }
+            }
+            if (n_keys > 0) load_v(base, n_keys);
+        }
+
+        // the warps' results side by side, then joined
+        __syncthreads();  // the previous piece's have been read
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+                const int h = 8 * n + 2 * t + e;
+                float* dst = s_o + ((size_t)warp * S::HB + h) * D;
+#pragma unroll
+                for (int c = 0; c < S::VC; ++c) {
+#pragma unroll
+                    for (int w = 0; w < S::VW; ++w)
+                        *reinterpret_cast<float2*>(dst + 16 * S::VW * c + 2 * S::VW * g + 2 * w) =
+                            make_float2(o[n][c * S::VW + w][e], o[n][c * S::VW + w][e + 2]);
+                }
+                if (g == 0) {
+                    s_m[warp * S::HB + h] = m[n][e];
+                    s_l[warp * S::HB + h] = l[n][e];
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = first == 0 && last == tiles;
+        if (!whole) {
+            if (first == 0) starting = (b * a.Hkv + hk) * a.hblocks + hb;
+            else continuing = last == tiles ? 2 : 1;
+        }
+        float* piece = a.part + ((size_t)cta * 2 + (first == 0 ? 1 : 0)) * S::PIECE;
+        for (int i = tid; i < heads * (D / 2); i += kAttnThreads) {
+            const int h = i / (D / 2), c = 2 * (i - h * (D / 2));
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, s_m[w * S::HB + h]);
+            float sum = 0.0f, y0 = 0.0f, y1 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float mw = s_m[w * S::HB + h];
+                const float f = mw == -INFINITY ? 0.0f : exp2f(mw - top);
+                const float2 x = *reinterpret_cast<const float2*>(s_o + ((size_t)w * S::HB + h) * D + c);
+                sum += f * s_l[w * S::HB + h];
+                y0 += f * x.x;
+                y1 += f * x.y;
+            }
+            if (whole) {
+                const size_t y = ((size_t)b * a.Hq + h0 + h) * D + c;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // no key left: zeros
+                st1(a.y, a.y_dt, y, y0 * inv);
+                st1(a.y, a.y_dt, y + 1, y1 * inv);
+            } else {
+                *reinterpret_cast<float2*>(piece + h * D + c) = make_float2(y0, y1);
+                if (c == 0) *reinterpret_cast<float2*>(piece + S::HB * D + 2 * h) = make_float2(top, sum);
+            }
+        }
+        at += last - first;
+    }
+    if (tid == 0) {
+        a.meta[2 * cta] = starting;
+        a.meta[2 * cta + 1] = continuing;
+    }
+}
+
+// Joins the pieces of a (row, key head, head block) that several CTAs share.  CTA x looks at the piece that
+// CTA x of the first kernel started, blockIdx.y at `per` heads of it; warps beyond the heads take every
+// (warps / per)-th piece.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnDecodeArgs a, int ctas, int per) {
+    using S = AttnShape<D, NT>;
+    constexpr int E = D / 32;  // channels of a lane
+    __shared__ float s_o[8][D], s_m[8], s_l[8];
+    const int row = a.meta[2 * blockIdx.x];
+    if (row < 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int hb = row % a.hblocks, hk = row / a.hblocks % a.Hkv, b = row / a.hblocks / a.Hkv;
+    const int heads = min(S::HB, a.group - hb * S::HB);
+    int pieces = 1;  // the starting one, then continuing ones up to the one that ends
+    while (blockIdx.x + pieces < (unsigned)ctas) {
+        const int kind = a.meta[2 * (blockIdx.x + pieces) + 1];
+        if (kind == 0) break;
+        ++pieces;
+        if (kind == 2) break;
+    }
+    const int strides = 8 / per;
+    const int h = blockIdx.y * per + warp % per, sub = warp / per;
+    float top = -INFINITY, sum = 0.0f, y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = 0.0f;
+    if (h < heads) {
+        for (int i = sub; i < pieces; i += strides) {
+            const float* piece = a.part + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * S::PIECE;
+            const float mi = piece[S::HB * D + 2 * h], li = piece[S::HB * D + 2 * h + 1];
+            if (mi == -INFINITY && li == 0.0f) continue;
+            const float next = fmaxf(top, mi);
+            const float f0 = top == -INFINITY ? 0.0f : exp2f(top - next), f1 = mi == -INFINITY ? 1.0f : exp2f(mi - next);
+            top = next;
+            sum = sum * f0 + li * f1;
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] = y[e] * f0 + piece[h * D + lane + 32 * e] * f1;
+        }
+    }
+    if (strides > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = y[e];
+        if (lane == 0) {
+            s_m[warp] = top;
+            s_l[warp] = sum;
+        }
+        __syncthreads();
+        if (sub == 0) {
+            for (int s = 1; s < strides; ++s) {
+                const int w = s * per + warp;
+                const float mi = s_m[w], li = s_l[w];
+                if (mi == -INFINITY && li == 0.0f) continue;
+                const float next = fmaxf(top, mi);
+                const float f0 = top == -INFINITY ? 0.0f : exp2f(top - next), f1 = mi == -INFINITY ? 1.0f : exp2f(mi - next);
+                top = next;
+                sum = sum * f0 + li * f1;
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = y[e] * f0 + s_o[w][lane + 32 * e] * f1;
+            }
+        }
+    }
+    if (sub == 0 && h < heads) {
+        const size_t at = ((size_t)b * a.Hq + hk * a.group + hb * S::HB + h) * D;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // no key left: zeros
+#pragma unroll
+        for (int e = 0; e < E; ++e) st1(a.y, a.y_dt, at + lane + 32 * e, y[e] * inv);
+    }
+}
+
+}  // namespace gdn

@@ -17,6 +17,7 @@ enum ErrBits : unsigned {
     kErrSeqlens = 2u,      // cu_seqlens not non-decreasing / out of [0, N]
     kErrSlot = 4u,         // a decode row named a state slot out of range
     kErrBounds = 8u,       // bounds-checking build: a computed global index fell outside its tensor
+    kErrPage = 16u,        // a page table entry, page list or length named no page of the cache
 };
 
 __device__ unsigned int g_error_word;

@@ -358,6 +358,9 @@ gdn_status_t gdn_check_device_error(gdn_stream_t stream) {
         if (word & gdn::kErrTimeout) return fail(GDN_ERR_TIMEOUT, "a device-side wait ran out (word 0x%x)", word);
         if (word & gdn::kErrSeqlens) return fail(GDN_ERR_INVALID_ARG, "cu_seqlens out of order or range (word 0x%x)", word);
         if (word & gdn::kErrSlot) return fail(GDN_ERR_INVALID_ARG, "state_slot out of range (word 0x%x)", word);
+        if (word & gdn::kErrPage)
+            return fail(GDN_ERR_INVALID_ARG, "a page table entry, page list or length names no page of the cache (word 0x%x)",
+                        word);
         if (word & gdn::kErrBounds)
             return fail(GDN_ERR_INVALID_ARG, "a device-side bounds check failed: an index outside its tensor (word 0x%x)", word);
         return fail(GDN_ERR_CUDA, "device error word 0x%x", word);
@@ -766,3 +769,5 @@ gdn_status_t gdn_timing_stop(int cap, const char** names, int* launches, double*
 }
 
 }  // extern "C"
+
+#include "attn_api.cuh"

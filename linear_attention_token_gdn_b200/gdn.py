@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -24,6 +25,7 @@ _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 # Every symbol include/gdn.h declares, with its ctypes signature.
 _P, _I, _F, _Z, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint64
+_L = ctypes.c_int64
 SIGNATURES = {
     "gdn_version": ([], _I),
     "gdn_status_string": ([_I], ctypes.c_char_p),
@@ -52,6 +54,17 @@ SIGNATURES = {
                        ctypes.c_size_t, _P], _I),
     "gdn_chunk_fwd_prep": ([_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _F, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I,
                             _I, _P, _P, _P, ctypes.c_size_t, _P], _I),
+    "gdn_attn_prep": ([_P, _P, _L, _L, _P, _P, _F, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P], _I),
+    "gdn_attn_prep_cache": ([_P, _P, _P, _L, _L, _L, _P, _P, _F, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _I, _I, _I, _I, _I,
+                             _P, _P, _P, _P], _I),
+    "gdn_attn_prep_bwd_workspace_size": ([_I], _Z),
+    "gdn_attn_prep_bwd": ([_P, _P, _P, _P, _L, _L, _P, _P, _F, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _Z,
+                           _P], _I),
+    "gdn_attn_decode_workspace_size": ([_I, _I, _I], _Z),
+    "gdn_attn_decode": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P, _P, _Z, _P], _I),
+    "gdn_attn_page_mean": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P], _I),
+    "gdn_attn_select_workspace_size": ([_I, _I, _I], _Z),
+    "gdn_attn_select": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _Z, _P], _I),
     "gdn_timing_start": ([_I], _I),
     "gdn_timing_stop": ([_I, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(_I), ctypes.POINTER(ctypes.c_double),
                          ctypes.POINTER(_I)], _I),
@@ -385,3 +398,192 @@ def out_gate(y, z, norm_w, eps=1e-6, out=None, stream=None):
     _check(lib().gdn_out_gate(_ptr(y), _ptr(z), _ptr(norm_w), float(eps), N, H, dv, _dt(y), _dt(z), _ptr(out),
                               _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- the attention layer's operators
+
+
+def _on_stream(fn):
+    """Runs ``fn`` with the first tensor's device current and, where one is given, ``stream`` as its current
+    stream, so that what it allocates and launches belongs to that stream."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kwargs):
+        device = first.device
+        if device.type != "cuda":
+            raise ValueError("libgdn takes device tensors only")
+        if stream is None and device.index == torch.cuda.current_device():
+            return fn(first, *args, **kwargs)
+        with torch.cuda.device(device), torch.cuda.stream(stream):
+            return fn(first, *args, **kwargs)
+    return call
+
+
+def _now():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _arg(name, t, device, dtype, shape):
+    """Address of a contiguous tensor of this type, shape and device."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} is not a contiguous {dtype} tensor of shape {list(shape)} on {device}: "
+                         f"{t.dtype} {list(t.shape)}, strides {list(t.stride())}, on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(name, t, like, heads=None):
+    """(address, token stride) of [N, H, d] rows: a token's heads contiguous, tokens any stride apart."""
+    N, H, d = t.shape
+    if t.dtype != like.dtype or t.device != like.device or N != like.shape[0] or d != like.shape[2] \
+            or (heads is not None and H != heads):
+        raise ValueError(f"{name} does not go with the other rows: {t.dtype} {list(t.shape)} on {t.device}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d != 1) or (s1 != d and H != 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous (strides {s0}, {s1}, {s2})")
+    return t.data_ptr(), s0 if N > 1 else H * d
+
+
+def _angles(inv_freq, device):
+    """(address, rot_dim) of the rotation's frequencies."""
+    if inv_freq is None or inv_freq.numel() == 0:
+        return None, 0
+    return _arg("inv_freq", inv_freq, device, torch.float64, (inv_freq.numel(),)), 2 * inv_freq.numel()
+
+
+def _room(workspace, nbytes, device):
+    """The caller's workspace, or a new one."""
+    if workspace is None:
+        return torch.empty(nbytes, device=device, dtype=torch.uint8)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("the workspace is not a contiguous tensor on the call's device")
+    return workspace
+
+
+def _size(t):
+    return t.numel() * t.element_size()
+
+
+@_on_stream
+def attn_prep(q, k, w_q, w_k, positions, inv_freq, eps=1e-6, out_dtype=None, out=None):
+    """gdn_attn_prep: zero-centred RMSNorm and rotation of query and key heads.  q [N, Hq, d] and k [N, Hkv, d] may be
+    slices of one projection's output; inv_freq [rot_dim / 2] fp64 (None: no rotation).  Returns (q_out, k_out)."""
+    N, Hq, d = q.shape
+    Hkv, dev = k.shape[1], q.device
+    qp, qs = _rows("q", q, q)
+    kp, ks = _rows("k", k, q)
+    fp, rot = _angles(inv_freq, dev)
+    if out is None:
+        out_dtype = q.dtype if out_dtype is None else out_dtype
+        out = torch.empty(N, Hq, d, device=dev, dtype=out_dtype), torch.empty(N, Hkv, d, device=dev, dtype=out_dtype)
+    q_out, k_out = out
+    _check(lib().gdn_attn_prep(qp, kp, qs, ks, _arg("w_q", w_q, dev, torch.float32, (d,)),
+                               _arg("w_k", w_k, dev, torch.float32, (d,)), eps,
+                               _arg("positions", positions, dev, torch.int32, (N,)), fp, rot, N, Hq, Hkv, d, _dt(q),
+                               _dt(q_out), _arg("q_out", q_out, dev, q_out.dtype, (N, Hq, d)),
+                               _arg("k_out", k_out, dev, q_out.dtype, (N, Hkv, d)), _now()))
+    return q_out, k_out
+
+
+@_on_stream
+def attn_prep_cache(q, k, v, w_q, w_k, positions, inv_freq, k_cache, v_cache, page_table, cu_seqlens=None, eps=1e-6,
+                    q_out=None):
+    """gdn_attn_prep_cache: attn_prep with the keys and the values v [N, Hkv, d] written to the paged cache
+    [num_pages, Hkv, page_size, d] in place; row b of page_table [num_seqs, max_pages] holds sequence b's pages.
+    Without cu_seqlens every row has N / num_seqs tokens.  Returns q_out (in the cache's dtype)."""
+    N, Hq, d = q.shape
+    Hkv, dev = k.shape[1], q.device
+    num_pages, _, page_size, _ = k_cache.shape
+    num_seqs, max_pages = page_table.shape
+    qp, qs = _rows("q", q, q)
+    kp, ks = _rows("k", k, q)
+    vp, vs = _rows("v", v, q, Hkv)
+    fp, rot = _angles(inv_freq, dev)
+    dtype = k_cache.dtype
+    if q_out is None:
+        q_out = torch.empty(N, Hq, d, device=dev, dtype=dtype)
+    cache = (num_pages, Hkv, page_size, d)
+    _check(lib().gdn_attn_prep_cache(
+        qp, kp, vp, qs, ks, vs, _arg("w_q", w_q, dev, torch.float32, (d,)), _arg("w_k", w_k, dev, torch.float32, (d,)), eps,
+        _arg("positions", positions, dev, torch.int32, (N,)), fp, rot,
+        None if cu_seqlens is None else _arg("cu_seqlens", cu_seqlens, dev, torch.int32, (num_seqs + 1,)), num_seqs, N, Hq,
+        Hkv, d, _arg("page_table", page_table, dev, torch.int32, (num_seqs, max_pages)), max_pages, num_pages, page_size,
+        _dt(q), _dt(k_cache), _arg("q_out", q_out, dev, dtype, (N, Hq, d)), _arg("k_cache", k_cache, dev, dtype, cache),
+        _arg("v_cache", v_cache, dev, dtype, cache), _now()))
+    return q_out
+
+
+@_on_stream
+def attn_prep_bwd(dq_out, dk_out, q, k, w_q, w_k, positions, inv_freq, eps=1e-6, out=None, workspace=None):
+    """gdn_attn_prep_bwd: gradients of attn_prep for its own inputs.  Returns dict(dq, dk, dw_q, dw_k): dq, dk contiguous
+    in q's dtype, dw_q, dw_k [d] fp32."""
+    N, Hq, d = q.shape
+    Hkv, dev = k.shape[1], q.device
+    qp, qs = _rows("q", q, q)
+    kp, ks = _rows("k", k, q)
+    fp, rot = _angles(inv_freq, dev)
+    if out is None:
+        out = dict(dq=torch.empty(N, Hq, d, device=dev, dtype=q.dtype), dk=torch.empty(N, Hkv, d, device=dev, dtype=q.dtype),
+                   dw_q=torch.empty(d, device=dev), dw_k=torch.empty(d, device=dev))
+    workspace = _room(workspace, lib().gdn_attn_prep_bwd_workspace_size(d), dev)
+    _check(lib().gdn_attn_prep_bwd(
+        _arg("dq_out", dq_out, dev, dq_out.dtype, (N, Hq, d)), _arg("dk_out", dk_out, dev, dq_out.dtype, (N, Hkv, d)), qp, kp,
+        qs, ks, _arg("w_q", w_q, dev, torch.float32, (d,)), _arg("w_k", w_k, dev, torch.float32, (d,)), eps,
+        _arg("positions", positions, dev, torch.int32, (N,)), fp, rot, N, Hq, Hkv, d, _dt(q), _dt(dq_out),
+        _arg("dq", out["dq"], dev, q.dtype, (N, Hq, d)), _arg("dk", out["dk"], dev, q.dtype, (N, Hkv, d)),
+        _arg("dw_q", out["dw_q"], dev, torch.float32, (d,)), _arg("dw_k", out["dw_k"], dev, torch.float32, (d,)),
+        workspace.data_ptr(), _size(workspace), _now()))
+    return out
+
+
+@_on_stream
+def attn_decode(q, k_cache, v_cache, page_table, lens, pages=None, scale=None, y_dtype=None, y=None, workspace=None):
+    """gdn_attn_decode: attention of one new token per row, q [B, Hq, d], over the first lens[b] positions of the row's
+    pages, or over the listed logical pages [B, Hkv, n_sel] of each key head.  scale defaults to d ** -0.5.  Returns y."""
+    B, Hq, d = q.shape
+    num_pages, Hkv, page_size, _ = k_cache.shape
+    max_pages, dev = page_table.shape[1], q.device
+    if y is None:
+        y = torch.empty(B, Hq, d, device=dev, dtype=q.dtype if y_dtype is None else y_dtype)
+    workspace = _room(workspace, lib().gdn_attn_decode_workspace_size(Hq, Hkv, d), dev)
+    cache, n_sel = (num_pages, Hkv, page_size, d), 0 if pages is None else pages.shape[2]
+    _check(lib().gdn_attn_decode(
+        _arg("q", q, dev, q.dtype, (B, Hq, d)), _arg("k_cache", k_cache, dev, q.dtype, cache),
+        _arg("v_cache", v_cache, dev, q.dtype, cache), _arg("page_table", page_table, dev, torch.int32, (B, max_pages)),
+        _arg("lens", lens, dev, torch.int32, (B,)),
+        None if pages is None else _arg("pages", pages, dev, torch.int32, (B, Hkv, n_sel)), n_sel, B, Hq, Hkv, d, max_pages,
+        num_pages, page_size, d ** -0.5 if scale is None else scale, _dt(q), _dt(y), _arg("y", y, dev, y.dtype, (B, Hq, d)),
+        workspace.data_ptr(), _size(workspace), _now()))
+    return y
+
+
+@_on_stream
+def attn_page_mean(k_cache, page_table, lens, page_mean=None, starts=None):
+    """gdn_attn_page_mean: the mean key of each page that holds a position in [starts[b], lens[b]) (starts None: 0), into
+    page_mean [num_pages, Hkv, d] fp32 in place (None: a new one of zeros).  Returns page_mean."""
+    num_pages, Hkv, page_size, d = k_cache.shape
+    (B, max_pages), dev = page_table.shape, k_cache.device
+    if page_mean is None:
+        page_mean = torch.zeros(num_pages, Hkv, d, device=dev)
+    _check(lib().gdn_attn_page_mean(
+        _arg("k_cache", k_cache, dev, k_cache.dtype, (num_pages, Hkv, page_size, d)),
+        _arg("page_table", page_table, dev, torch.int32, (B, max_pages)), _arg("lens", lens, dev, torch.int32, (B,)),
+        None if starts is None else _arg("starts", starts, dev, torch.int32, (B,)), B, Hkv, d, max_pages, num_pages, page_size,
+        _dt(k_cache), _arg("page_mean", page_mean, dev, torch.float32, (num_pages, Hkv, d)), _now()))
+    return page_mean
+
+
+@_on_stream
+def attn_select(q, page_mean, page_table, lens, page_size, n_sel, n_first=0, n_last=1, pages=None, workspace=None):
+    """gdn_attn_select: for each row and key head the n_sel logical pages with the highest score of their mean key, the
+    first n_first and last n_last always among them; ascending, -1 behind the last.  Returns pages [B, Hkv, n_sel] int32."""
+    B, Hq, d = q.shape
+    num_pages, Hkv, _ = page_mean.shape
+    max_pages, dev = page_table.shape[1], q.device
+    if pages is None:
+        pages = torch.empty(B, Hkv, n_sel, device=dev, dtype=torch.int32)
+    workspace = _room(workspace, lib().gdn_attn_select_workspace_size(B, Hkv, max_pages), dev)
+    _check(lib().gdn_attn_select(
+        _arg("q", q, dev, q.dtype, (B, Hq, d)), _arg("page_mean", page_mean, dev, torch.float32, (num_pages, Hkv, d)),
+        _arg("page_table", page_table, dev, torch.int32, (B, max_pages)), _arg("lens", lens, dev, torch.int32, (B,)), B, Hq,
+        Hkv, d, max_pages, num_pages, page_size, n_sel, n_first, n_last, _dt(q),
+        _arg("pages", pages, dev, torch.int32, (B, Hkv, n_sel)), workspace.data_ptr(), _size(workspace), _now()))
+    return pages

@@ -19,6 +19,8 @@ Every function follows "On the design of Qwen3.8-Next architecture"
 * :func:`mixer`       -- prep -> recurrence -> out_gate in fp64 (optionally with q, k, v
   rounded once to a 16-bit storage format between prep and the recurrence,
   :func:`round_to_format`).
+* :func:`attn_prep`, :func:`attn_prep_backward`, :func:`attn_decode`, :func:`page_mean`,
+  :func:`attn_select` -- the attention layer's operators (``attention.py``).
 
 The pins that tie these functions to the page (closed form eq. (5), pure decay,
 exact retrieval, brute-force products, textbook special cases, a hand-worked
@@ -32,6 +34,8 @@ import subprocess
 import threading
 
 import numpy as np
+
+from .attention import attn_decode, attn_prep, attn_prep_backward, attn_select, page_mean  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _SRC = os.path.join(_HERE, "gdn_oracle.c")
