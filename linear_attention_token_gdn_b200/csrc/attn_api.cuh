@@ -57,6 +57,25 @@ long long span_bytes(long long n, long long stride, long long width, int dt) {
         REQUIRE((long long)max_pages * page_size <= (1LL << 30), "max_pages * page_size above 2^30");       \
     } while (0)
 
+// A launch that may start while the kernel before it on the stream still runs; it waits for that kernel itself.
+template <class... P, class... A>
+gdn_status_t launch_after(const char* name, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t st, const A&... args) {
+    gdn::LaunchScope timed(st, name);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? GDN_OK : fail(GDN_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+}
+
 // ---------------------------------------------------------------- norm and rotation
 
 // Heads per unit: the most (up to 8) that still give every SM about two blocks.
@@ -89,7 +108,7 @@ gdn_status_t attn_prep_launch(gdn::AttnPrepArgs& a, int d, int in_dt, cudaStream
     a.hps = attn_heads_per_unit((long long)a.N * (a.Hq + (CACHE ? 2 : 1) * a.Hkv), lanes, a.Hq, dev.sms);
     a.cq = (a.Hq + a.hps - 1) / a.hps;
     a.ck = (a.Hkv + a.hps - 1) / a.hps;
-    const long long threads = (long long)a.N * (a.cq + (CACHE ? 2 : 1) * a.ck) * lanes;
+    const long long threads = (long long)a.N * (a.cq + a.ck) * lanes;
     const long long grid = (threads + gdn::kAttnPrepThreads - 1) / gdn::kAttnPrepThreads;
     REQUIRE(grid * (gdn::kAttnPrepThreads / lanes) < (1LL << 31) && threads < (1LL << 32) - 256, "N=%d with Hq=%d too large",
             a.N, a.Hq);
@@ -98,17 +117,24 @@ gdn_status_t attn_prep_launch(gdn::AttnPrepArgs& a, int d, int in_dt, cudaStream
     return attn_prep_go<gdn::kF16, CACHE>(d, a, (unsigned)grid, st);
 }
 
-template <int IN>
+template <int IN, int DY>
 gdn_status_t attn_prep_bwd_go(int d, const gdn::AttnPrepBwdArgs& a, unsigned grid, cudaStream_t st) {
     gdn::LaunchScope timed(st, "attn_prep_bwd_kernel");
     switch (d) {
-        case 16: gdn::attn_prep_bwd_kernel<IN, 16><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
-        case 32: gdn::attn_prep_bwd_kernel<IN, 32><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
-        case 64: gdn::attn_prep_bwd_kernel<IN, 64><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
-        case 128: gdn::attn_prep_bwd_kernel<IN, 128><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
-        default: gdn::attn_prep_bwd_kernel<IN, 256><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        case 16: gdn::attn_prep_bwd_kernel<IN, 16, DY><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        case 32: gdn::attn_prep_bwd_kernel<IN, 32, DY><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        case 64: gdn::attn_prep_bwd_kernel<IN, 64, DY><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        case 128: gdn::attn_prep_bwd_kernel<IN, 128, DY><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
+        default: gdn::attn_prep_bwd_kernel<IN, 256, DY><<<grid, gdn::kAttnPrepThreads, 0, st>>>(a); break;
     }
     return launched("attn_prep_bwd_kernel");
+}
+
+template <int IN>
+gdn_status_t attn_prep_bwd_dy(int d, int dy, const gdn::AttnPrepBwdArgs& a, unsigned grid, cudaStream_t st) {
+    if (dy == GDN_F32) return attn_prep_bwd_go<IN, gdn::kF32>(d, a, grid, st);
+    if (dy == GDN_BF16) return attn_prep_bwd_go<IN, gdn::kBF16>(d, a, grid, st);
+    return attn_prep_bwd_go<IN, gdn::kF16>(d, a, grid, st);
 }
 
 constexpr int kAttnBwdBlocks = 2048;  // most blocks of the gradient kernel: sizes its workspace
@@ -134,18 +160,13 @@ gdn_status_t attn_decode_run(const gdn::AttnDecodeArgs& a, const DeviceInfo& dev
     }
     int ctas = dev.sms * per_sm.load(std::memory_order_relaxed);
     if (ctas > gdn::kAttnMaxCtas) ctas = gdn::kAttnMaxCtas;
-    {
-        gdn::LaunchScope timed(st, "attn_decode_kernel");
-        kernel<<<(unsigned)ctas, gdn::kAttnThreads, S::SMEM, st>>>(a);
-        gdn_status_t r = launched("attn_decode_kernel");
-        if (r != GDN_OK) return r;
-    }
+    gdn_status_t r = launch_after("attn_decode_kernel", kernel, dim3((unsigned)ctas), dim3(gdn::kAttnThreads), S::SMEM, st, a);
+    if (r != GDN_OK) return r;
     // few work rows: many pieces each, so one head per block and eight warps over its pieces
     const bool spread = (long long)a.B * a.Hkv * a.hblocks * 4 < ctas;
     const int per = spread ? 1 : 8;
-    gdn::LaunchScope timed(st, "attn_join_kernel");
-    gdn::attn_join_kernel<D, NT><<<dim3((unsigned)ctas, (unsigned)(S::HB / per)), 256, 0, st>>>(a, ctas, per);
-    return launched("attn_join_kernel");
+    return launch_after("attn_join_kernel", gdn::attn_join_kernel<D, NT>, dim3((unsigned)ctas, (unsigned)(S::HB / per)), dim3(256),
+                        0, st, a, ctas, per);
 }
 
 template <bool BF, int D>
@@ -177,23 +198,21 @@ int attn_head_tiles(int group, int d) { return group > 8 && d < 256 ? 2 : 1; }
 constexpr size_t kAttnMetaBytes = (size_t)gdn::kAttnMaxCtas * 2 * sizeof(int);
 
 template <bool BF>
-void attn_mean_launch(int d, const gdn::AttnMeanArgs& a, unsigned grid, cudaStream_t st) {
-    switch (d) {
-        case 32: gdn::attn_page_mean_kernel<BF, 32><<<grid, gdn::kMeanThreads, 0, st>>>(a); break;
-        case 64: gdn::attn_page_mean_kernel<BF, 64><<<grid, gdn::kMeanThreads, 0, st>>>(a); break;
-        case 128: gdn::attn_page_mean_kernel<BF, 128><<<grid, gdn::kMeanThreads, 0, st>>>(a); break;
-        default: gdn::attn_page_mean_kernel<BF, 256><<<grid, gdn::kMeanThreads, 0, st>>>(a); break;
-    }
+gdn_status_t attn_mean_launch(int d, const gdn::AttnMeanArgs& a, unsigned grid, cudaStream_t st) {
+    auto* kernel = d == 32    ? gdn::attn_page_mean_kernel<BF, 32>
+                   : d == 64  ? gdn::attn_page_mean_kernel<BF, 64>
+                   : d == 128 ? gdn::attn_page_mean_kernel<BF, 128>
+                              : gdn::attn_page_mean_kernel<BF, 256>;
+    return launch_after("attn_page_mean_kernel", kernel, dim3(grid), dim3(gdn::kMeanThreads), 0, st, a);
 }
 
 template <bool BF>
-void attn_score_launch(int d, const gdn::AttnSelectArgs& a, unsigned grid, cudaStream_t st) {
-    switch (d) {
-        case 32: gdn::attn_score_kernel<BF, 32><<<grid, gdn::kScoreThreads, 0, st>>>(a); break;
-        case 64: gdn::attn_score_kernel<BF, 64><<<grid, gdn::kScoreThreads, 0, st>>>(a); break;
-        case 128: gdn::attn_score_kernel<BF, 128><<<grid, gdn::kScoreThreads, 0, st>>>(a); break;
-        default: gdn::attn_score_kernel<BF, 256><<<grid, gdn::kScoreThreads, 0, st>>>(a); break;
-    }
+gdn_status_t attn_score_launch(int d, const gdn::AttnSelectArgs& a, unsigned grid, cudaStream_t st) {
+    auto* kernel = d == 32    ? gdn::attn_score_kernel<BF, 32>
+                   : d == 64  ? gdn::attn_score_kernel<BF, 64>
+                   : d == 128 ? gdn::attn_score_kernel<BF, 128>
+                              : gdn::attn_score_kernel<BF, 256>;
+    return launch_after("attn_score_kernel", kernel, dim3(grid), dim3(gdn::kScoreThreads), 0, st, a);
 }
 
 }  // namespace
@@ -329,7 +348,7 @@ gdn_status_t gdn_attn_prep_bwd(const void* dq_out, const void* dk_out, const voi
     gdn::AttnPrepBwdArgs a{};
     a.q = q; a.k = k; a.dyq = dq_out; a.dyk = dk_out; a.q_stride = q_stride; a.k_stride = k_stride;
     a.w_q = w_q; a.w_k = w_k; a.eps = eps; a.positions = positions; a.inv_freq = inv_freq; a.rot = rot_dim;
-    a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.dy_dt = (int)dy_dtype; a.dq = dq; a.dk = dk;
+    a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.dq = dq; a.dk = dk;
     a.partial = reinterpret_cast<float*>(workspace);
     a.hps = attn_heads_per_unit((long long)N * (Hq + Hkv), lanes, Hq, dev.sms);
     a.cq = (Hq + a.hps - 1) / a.hps;
@@ -345,14 +364,12 @@ gdn_status_t gdn_attn_prep_bwd(const void* dq_out, const void* dk_out, const voi
     if (bk > (uk + subs - 1) / subs) bk = (uk + subs - 1) / subs;
     a.gq = (int)bq;
     const unsigned blocks = (unsigned)(bq + bk);
-    if (in_dtype == GDN_F32) r = attn_prep_bwd_go<gdn::kF32>(d, a, blocks, st);
-    else if (in_dtype == GDN_BF16) r = attn_prep_bwd_go<gdn::kBF16>(d, a, blocks, st);
-    else r = attn_prep_bwd_go<gdn::kF16>(d, a, blocks, st);
+    if (in_dtype == GDN_F32) r = attn_prep_bwd_dy<gdn::kF32>(d, (int)dy_dtype, a, blocks, st);
+    else if (in_dtype == GDN_BF16) r = attn_prep_bwd_dy<gdn::kBF16>(d, (int)dy_dtype, a, blocks, st);
+    else r = attn_prep_bwd_dy<gdn::kF16>(d, (int)dy_dtype, a, blocks, st);
     if (r != GDN_OK) return r;
-    gdn::LaunchScope timed(st, "attn_prep_dw_kernel");
-    gdn::attn_prep_dw_kernel<<<dim3(2, (unsigned)((d + 31) / 32)), dim3(32, 8), 0, st>>>(a.partial, a.gq, (int)blocks, d,
-                                                                                         dw_q, dw_k);
-    return launched("attn_prep_dw_kernel");
+    return launch_after("attn_prep_dw_kernel", gdn::attn_prep_dw_kernel, dim3(2, (unsigned)((d + 31) / 32)), dim3(32, 32), 0, st,
+                        (const float*)a.partial, a.gq, (int)blocks, d, dw_q, dw_k);
 }
 
 size_t gdn_attn_decode_workspace_size(int Hq, int Hkv, int d) {
@@ -421,10 +438,7 @@ gdn_status_t gdn_attn_page_mean(const void* k_cache, const int32_t* page_table, 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const long long most = (long long)B * Hkv * max_pages;  // units at most
     const unsigned grid = (unsigned)(most < 8LL * dev.sms ? most : 8LL * dev.sms);
-    gdn::LaunchScope timed(st, "attn_page_mean_kernel");
-    if (dtype == GDN_BF16) attn_mean_launch<true>(d, a, grid, st);
-    else attn_mean_launch<false>(d, a, grid, st);
-    return launched("attn_page_mean_kernel");
+    return dtype == GDN_BF16 ? attn_mean_launch<true>(d, a, grid, st) : attn_mean_launch<false>(d, a, grid, st);
 }
 
 size_t gdn_attn_select_workspace_size(int B, int Hkv, int max_pages) {
@@ -461,15 +475,11 @@ gdn_status_t gdn_attn_select(const void* q, const float* page_mean, const int32_
     if (max_pages > n_sel) {  // else every row has all its pages chosen
         const long long most = (long long)B * Hkv * ((max_pages + gdn::kScorePages - 1) / gdn::kScorePages);
         const unsigned grid = (unsigned)(most < 4LL * dev.sms ? most : 4LL * dev.sms);
-        gdn::LaunchScope timed(st, "attn_score_kernel");
-        if (dtype == GDN_BF16) attn_score_launch<true>(d, a, grid, st);
-        else attn_score_launch<false>(d, a, grid, st);
-        r = launched("attn_score_kernel");
+        r = dtype == GDN_BF16 ? attn_score_launch<true>(d, a, grid, st) : attn_score_launch<false>(d, a, grid, st);
         if (r != GDN_OK) return r;
     }
-    gdn::LaunchScope timed(st, "attn_select_kernel");
-    gdn::attn_select_kernel<<<(unsigned)((long long)B * Hkv), gdn::kSelectThreads, 0, st>>>(a);
-    return launched("attn_select_kernel");
+    return launch_after("attn_select_kernel", gdn::attn_select_kernel, dim3((unsigned)((long long)B * Hkv)),
+                        dim3(gdn::kSelectThreads), 0, st, a);
 }
 
 }  // extern "C"

@@ -118,8 +118,8 @@ struct AttnDecodeArgs {
     float scale_log2;                           // scale * log2(e)
     int y_dt;
     void* y;
-    int* meta;                                  // [grid][2]: row of the starting piece (-1: none); continuing piece:
-                                                // 0 none, 1 goes on, 2 ends
+    int* meta;                                  // [grid][2]: the pair whose first piece this CTA holds (-1: none), and
+                                                // the number of its pieces, one per CTA from here on
     float* part;                                // [grid][2][8 NT][D + 2]: o, then m and l (log2 scale)
 };
 
@@ -178,6 +178,9 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
     const long long capacity = (long long)a.max_pages * a.page_size;
     const int cta = blockIdx.x;
 
+    tc::wait_prerequisites();
+    tc::launch_dependents();  // every CTA is resident: the join's take no place from them
+
     // rows without a key
     for (int b = cta; b < a.B; b += gridDim.x) {
         if (a.lens[b] <= 0)
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
         });
     long long at = share * cta;
     const long long end = at + share < place.total ? at + share : place.total;
-    int starting = -1, continuing = 0;
+    int starting = -1, pieces = 0;
 
     int b = place.b;
     long long row_base = place.before;                   // the line's index of b's first tile
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
         const int heads = min(S::HB, a.group - hb * S::HB);
         const int32_t* table = a.table + (size_t)b * a.max_pages;
         const int32_t* list = CHOSEN ? a.pages + ((size_t)b * a.Hkv + hk) * a.n_sel : nullptr;
-        const int pages = (len + a.page_size - 1) / a.page_size;
+        const int row_pages = (len + a.page_size - 1) / a.page_size;
 
         // Q as the B operand: lane (g, t) holds channels 32 c + 8 t ... + 7 of head g
         uint32_t qf[NT][S::KC][4];
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
             if (CHOSEN) {
                 page = list[page];
                 if (page < 0) return 0;                  // padding of the list
-                if (page >= pages) {
+                if (page >= row_pages) {
                     if (lane == 0) raise_error(kErrPage);
                     return 0;
                 }
@@ -405,9 +408,9 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
         }
         __syncthreads();
         const bool whole = first == 0 && last == tiles;
-        if (!whole) {
-            if (first == 0) starting = (b * a.Hkv + hk) * a.hblocks + hb;
-            else continuing = last == tiles ? 2 : 1;
+        if (!whole && first == 0) {
+            starting = (b * a.Hkv + hk) * a.hblocks + hb;
+            pieces = (int)((row_base + (long long)(pair + 1) * tiles - 1) / share) - cta + 1;
         }
         float* piece = a.part + ((size_t)cta * 2 + (first == 0 ? 1 : 0)) * S::PIECE;
         for (int i = tid; i < heads * (D / 2); i += kAttnThreads) {
@@ -439,75 +442,76 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
     }
     if (tid == 0) {
         a.meta[2 * cta] = starting;
-        a.meta[2 * cta + 1] = continuing;
+        a.meta[2 * cta + 1] = pieces;
     }
 }
 
-// Joins the pieces of a (row, key head, head block) that several CTAs share.  CTA x looks at the piece that
-// CTA x of the first kernel started, blockIdx.y at `per` heads of it; warps beyond the heads take every
-// (warps / per)-th piece.
+// Joins the pieces of a (row, key head, head block) that several CTAs share: y = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
+// M = max m_i.  CTA x looks at the pair whose first piece CTA x of the first kernel held, blockIdx.y at `per` heads of
+// it, with 8 / per warps a head, each taking every (8 / per)-th piece.  M and the weights' sum come first, from all pieces
+// at once, so that the loads of the o_i do not wait for one another.
 template <int D, int NT>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnDecodeArgs a, int ctas, int per) {
     using S = AttnShape<D, NT>;
-    constexpr int E = D / 32;  // channels of a lane
-    __shared__ float s_o[8][D], s_m[8], s_l[8];
-    const int row = a.meta[2 * blockIdx.x];
+    constexpr int E = D / 32, V = E < 4 ? E : 4;  // channels of a lane, of one load
+    __shared__ float s_o[8][D];
+    tc::wait_prerequisites();
+    const int row = a.meta[2 * blockIdx.x], pieces = min(a.meta[2 * blockIdx.x + 1], ctas - (int)blockIdx.x);
     if (row < 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int hb = row % a.hblocks, hk = row / a.hblocks % a.Hkv, b = row / a.hblocks / a.Hkv;
     const int heads = min(S::HB, a.group - hb * S::HB);
-    int pieces = 1;  // the starting one, then continuing ones up to the one that ends
-    while (blockIdx.x + pieces < (unsigned)ctas) {
-        const int kind = a.meta[2 * (blockIdx.x + pieces) + 1];
-        if (kind == 0) break;
-        ++pieces;
-        if (kind == 2) break;
-    }
     const int strides = 8 / per;
     const int h = blockIdx.y * per + warp % per, sub = warp / per;
+    const bool live = h < heads;
+    auto piece = [&](int i) { return a.part + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * S::PIECE; };
     float top = -INFINITY, sum = 0.0f, y[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) y[e] = 0.0f;
-    if (h < heads) {
-        for (int i = sub; i < pieces; i += strides) {
-            const float* piece = a.part + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * S::PIECE;
-            const float mi = piece[S::HB * D + 2 * h], li = piece[S::HB * D + 2 * h + 1];
-            if (mi == -INFINITY && li == 0.0f) continue;
-            const float next = fmaxf(top, mi);
-            const float f0 = top == -INFINITY ? 0.0f : exp2f(top - next), f1 = mi == -INFINITY ? 1.0f : exp2f(mi - next);
+    if (live) {
+        for (int i = lane; i < pieces; i += 32) {
+            const float2 ml = *reinterpret_cast<const float2*>(piece(i) + S::HB * D + 2 * h);
+            const float next = fmaxf(top, ml.x);
+            if (next != -INFINITY) sum = sum * exp2f(top - next) + (ml.x == -INFINITY ? 0.0f : ml.y * exp2f(ml.x - next));
             top = next;
-            sum = sum * f0 + li * f1;
+        }
+        const float mine = top;
 #pragma unroll
-            for (int e = 0; e < E; ++e) y[e] = y[e] * f0 + piece[h * D + lane + 32 * e] * f1;
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        sum = mine == -INFINITY ? 0.0f : sum * exp2f(mine - top);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll 4
+        for (int i = sub; i < pieces; i += strides) {
+            const float* p = piece(i);
+            const float m = p[S::HB * D + 2 * h], f = m == -INFINITY ? 0.0f : exp2f(m - top);
+#pragma unroll
+            for (int e = 0; e < E; e += V) {
+                float x[V];
+                if constexpr (V == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(p + h * D + 32 * e + 4 * lane);
+                else if constexpr (V == 2) *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p + h * D + 2 * lane);
+                else x[0] = p[h * D + lane];
+#pragma unroll
+                for (int u = 0; u < V; ++u) y[e + u] = fmaf(f, x[u], y[e + u]);
+            }
         }
     }
     if (strides > 1) {
 #pragma unroll
         for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = y[e];
-        if (lane == 0) {
-            s_m[warp] = top;
-            s_l[warp] = sum;
-        }
         __syncthreads();
         if (sub == 0) {
-            for (int s = 1; s < strides; ++s) {
-                const int w = s * per + warp;
-                const float mi = s_m[w], li = s_l[w];
-                if (mi == -INFINITY && li == 0.0f) continue;
-                const float next = fmaxf(top, mi);
-                const float f0 = top == -INFINITY ? 0.0f : exp2f(top - next), f1 = mi == -INFINITY ? 1.0f : exp2f(mi - next);
-                top = next;
-                sum = sum * f0 + li * f1;
+            for (int w = per + warp; w < 8; w += per) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) y[e] = y[e] * f0 + s_o[w][lane + 32 * e] * f1;
+                for (int e = 0; e < E; ++e) y[e] += s_o[w][lane + 32 * e];
             }
         }
     }
-    if (sub == 0 && h < heads) {
+    if (sub == 0 && live) {
         const size_t at = ((size_t)b * a.Hq + hk * a.group + hb * S::HB + h) * D;
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // no key left: zeros
 #pragma unroll
-        for (int e = 0; e < E; ++e) st1(a.y, a.y_dt, at + lane + 32 * e, y[e] * inv);
+        for (int e = 0; e < E; ++e) st1(a.y, a.y_dt, at + 32 * (e / V * V) + V * lane + e % V, y[e] * inv);
     }
 }
 

@@ -34,13 +34,16 @@ __device__ __forceinline__ int attn_touched(const AttnMeanArgs& a, int b, int& f
     return (len + a.page_size - 1) / a.page_size - first;
 }
 
-// HBM-bound: a CTA reads a page of one key head (page_size x D, contiguous) with 16-byte loads, all of them
-// in flight at once for pages of 64 keys of 128 channels, and adds in fp32 in a fixed order.
+// HBM-bound: a CTA takes one page of one key head (page_size x D, contiguous) after another with 16-byte loads, U of
+// them in flight per thread, which is all of a page of 64 keys of 128 channels.  The next page's loads are issued before
+// this one's sums are joined over the CTA, and its place in the cache is looked up one page earlier still, so memory
+// never waits for the join.  Sums are fp32, in a fixed order.
 template <bool BF, int D>
 __global__ void __launch_bounds__(kMeanThreads) attn_page_mean_kernel(const AttnMeanArgs a) {
     constexpr int LPR = D / 8, RPP = kMeanThreads / LPR, U = 8;  // lanes of a key, keys of a pass, passes in flight
-    __shared__ __align__(16) float s_sum[RPP][D];  // written 16 bytes at a time
+    __shared__ __align__(16) float s_sum[2][RPP][D];  // written 16 bytes at a time
     const int tid = threadIdx.x, l = tid % LPR, sub = tid / LPR;
+    tc::wait_prerequisites();
     long long share = 0;
     const AttnPlace place = attn_locate<kMeanThreads>(
         a.B,
@@ -52,35 +55,52 @@ __global__ void __launch_bounds__(kMeanThreads) attn_page_mean_kernel(const Attn
             share = (total + gridDim.x - 1) / gridDim.x;
             return share * blockIdx.x;
         });
-    long long at = share * blockIdx.x;
-    const long long end = min(at + share, place.total);
+    const long long end = min(share * blockIdx.x + share, place.total);
     int b = place.b, first = 0, n = 0;
     long long row_base = place.before;
-    if (at < end) n = attn_touched(a, b, first);
-    for (; at < end; ++at) {
+    if (share * blockIdx.x < end) n = attn_touched(a, b, first);
+    // Item `at` of the line: its (page, key head) in the cache, or -1, and its keys inside the row.
+    struct Item {
+        long long slot;
+        int count;
+    };
+    auto find = [&](long long at) -> Item {
+        Item it{-1, 0};
+        if (at >= end) return it;
         while (at >= row_base + (long long)n * a.Hkv) {
             row_base += (long long)n * a.Hkv;
             n = attn_touched(a, ++b, first);
         }
         const int i = (int)((at - row_base) / a.Hkv), hk = (int)(at - row_base - (long long)i * a.Hkv);
         const int page = first + i;
-        const int count = min(a.page_size, a.lens[b] - page * a.page_size);
+        it.count = min(a.page_size, a.lens[b] - page * a.page_size);
         const int phys = a.table[(size_t)b * a.max_pages + page];
-        if (phys < 0 || phys >= a.num_pages || count <= 0) {  // uniform
+        if (phys < 0 || phys >= a.num_pages || it.count <= 0) {  // uniform
             if (tid == 0) raise_error(kErrPage);
-            continue;
+            return it;
         }
-        const size_t slot = (size_t)phys * a.Hkv + hk;
-        if (!in_bounds((long long)slot, (long long)a.num_pages * a.Hkv)) continue;
-        const uint16_t* keys = reinterpret_cast<const uint16_t*>(a.k_cache) + slot * a.page_size * D + 8 * l;
-        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int r0 = sub; r0 < count; r0 += U * RPP) {
-            uint4 x[U];
+        it.slot = (long long)phys * a.Hkv + hk;
+        if (!in_bounds(it.slot, (long long)a.num_pages * a.Hkv)) it.slot = -1;
+        return it;
+    };
+    uint4 x[U];
+    const uint16_t* cache = reinterpret_cast<const uint16_t*>(a.k_cache) + 8 * l;
+    auto load = [&](const Item& it, int r0) {
+        const uint16_t* keys = cache + it.slot * a.page_size * D;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (r0 + u * RPP < count) x[u] = *reinterpret_cast<const uint4*>(keys + (size_t)(r0 + u * RPP) * D);
-            }
+        for (int u = 0; u < U; ++u) {
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (it.slot >= 0 && r0 + u * RPP < it.count) x[u] = *reinterpret_cast<const uint4*>(keys + (size_t)(r0 + u * RPP) * D);
+        }
+    };
+
+    long long at = share * blockIdx.x;
+    Item now = find(at), next = find(at + 1);
+    load(now, sub);
+    int parity = 0;
+    for (; at < end; ++at) {
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int r0 = sub;;) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
@@ -91,16 +111,24 @@ __global__ void __launch_bounds__(kMeanThreads) attn_page_mean_kernel(const Attn
                     sum[2 * e + 1] += f.y;
                 }
             }
+            r0 += U * RPP;
+            if (r0 >= now.count) break;
+            load(now, r0);
         }
-        __syncthreads();  // the previous page's sums have been read
-        stv<kF32, 8>(s_sum[sub], 8 * l, sum);
-        __syncthreads();
+        const Item done = now;
+        now = next;
+        load(now, sub);
+        next = find(at + 2);
+        if (done.slot < 0) continue;  // uniform
+        stv<kF32, 8>(s_sum[parity][sub], 8 * l, sum);
+        __syncthreads();  // the other buffer's readers have passed the sync before
         for (int c = tid; c < D; c += kMeanThreads) {
             float total = 0.0f;
 #pragma unroll
-            for (int r = 0; r < RPP; ++r) total += s_sum[r][c];
-            a.mean[slot * D + c] = total / (float)count;
+            for (int r = 0; r < RPP; ++r) total += s_sum[parity][r][c];
+            a.mean[done.slot * D + c] = total / (float)done.count;
         }
+        parity ^= 1;
     }
 }
 
@@ -115,7 +143,7 @@ struct AttnSelectArgs {
     int32_t* pages;                             // [B, Hkv, n_sel]
 };
 
-constexpr int kScoreThreads = 128, kScorePages = kScoreThreads, kScoreHeads = 8, kScoreSlab = 32;
+constexpr int kScoreThreads = 128, kScorePages = 16 * kScoreThreads / 32;  // 16 pages a warp
 
 // A double as an unsigned number of the same order; NaN is the lowest.
 __device__ __forceinline__ unsigned long long sort_key(double x) {
@@ -124,16 +152,24 @@ __device__ __forceinline__ unsigned long long sort_key(double x) {
     return bits < 0 ? ~(unsigned long long)bits : (unsigned long long)bits | 0x8000000000000000ull;
 }
 
-// One thread per page: 128 pages of a (row, key head) at a time, their means brought into shared memory 32
-// channels at a time (rows padded by 16 bytes: a quarter warp's 16-byte reads then cover all banks), 8 heads'
-// sums per thread.  Bound by the fp64 units: 8 fused multiply-adds per 4 bytes of mean key at a group of 8.
+__device__ __forceinline__ void dmma(double (&c)[2], double a, double b) {
+    asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0,%1}, {%2}, {%3}, {%0,%1};"
+                 : "+d"(c[0]), "+d"(c[1])
+                 : "d"(a), "d"(b));
+}
+
+// Scores of 64 pages of a (row, key head) at a time, 16 per warp in two 8 x 8 x 4 fp64 products, whose 8 columns are
+// query heads.  The contraction runs over channels in any order, so a lane's 4 channels of a page are one 16-byte load,
+// all of a page's loads (8 at d = 128) are in flight together, and nothing of the means goes through shared memory;
+// only the queries do, as doubles in fragment order, once per (row, key head).  Bound by HBM (the means) and by the
+// conversions to fp64, 16 a clock and SM: 4 us and 10 us of the 64-row case's 16800 pages of 8 key heads.
 template <bool BF, int D>
 __global__ void __launch_bounds__(kScoreThreads) attn_score_kernel(const AttnSelectArgs a) {
-    constexpr int ROW = kScoreSlab + 4;
-    __shared__ __align__(16) float s_mean[kScorePages][ROW];
-    __shared__ __align__(16) double s_q[D][kScoreHeads];
-    __shared__ int s_phys[kScorePages];
-    const int tid = threadIdx.x;
+    constexpr int CH = D < 128 ? D : 128, KB = CH / 16;  // channels in flight, 16-byte loads of a page for them
+    __shared__ double s_q[D / 4][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    tc::wait_prerequisites();
+    tc::launch_dependents();
     const long long capacity = (long long)a.max_pages * a.page_size;
     auto pages_of = [&](int b) { return (attn_len(a.lens, b, capacity) + a.page_size - 1) / a.page_size; };
     auto blocks_of = [&](int pages) { return pages > a.n_sel ? (pages + kScorePages - 1) / kScorePages : 0; };
@@ -146,74 +182,86 @@ __global__ void __launch_bounds__(kScoreThreads) attn_score_kernel(const AttnSel
         });
     long long at = share * blockIdx.x;
     const long long end = min(at + share, place.total);
-    int b = place.b, n = 0;
+    int b = place.b, pages = 0, n = 0, held = -1;  // held: the (row, key head) whose queries are in s_q
     long long row_base = place.before;
-    if (at < end) n = blocks_of(pages_of(b));
+    if (at < end) n = blocks_of(pages = pages_of(b));
     for (; at < end; ++at) {
         while (at >= row_base + (long long)n * a.Hkv) {
             row_base += (long long)n * a.Hkv;
-            n = blocks_of(pages_of(++b));
+            n = blocks_of(pages = pages_of(++b));
         }
         const int hk = (int)((at - row_base) / n);
-        const int page = (int)(at - row_base - (long long)hk * n) * kScorePages + tid;
-        const int pages = pages_of(b);
-        int phys = -1;
-        if (page < pages) phys = attn_page(a.table, a.max_pages, a.num_pages, b, page);
-        __syncthreads();  // the previous block's shared values have been read
-        s_phys[tid] = phys;
-        double best = -INFINITY;
-        bool any = false;
-        for (int h0 = 0; h0 < a.group; h0 += kScoreHeads) {
-            const int heads = min(kScoreHeads, a.group - h0);
-            if (h0 > 0) __syncthreads();
-            for (int i = tid; i < D * kScoreHeads; i += kScoreThreads) {
-                const int h = i / D, c = i - h * D;
-                s_q[c][h] = h < heads ? (double)ld1(a.q, BF ? kBF16 : kF16,
-                                                    ((size_t)b * a.Hq + hk * a.group + h0 + h) * D + c)
-                                      : 0.0;
-            }
-            double sum[kScoreHeads];
+        const int page0 = (int)(at - row_base - (long long)hk * n) * kScorePages + warp * 16 + g;
+        const float* mean[2];
 #pragma unroll
-            for (int h = 0; h < kScoreHeads; ++h) sum[h] = 0.0;
-            for (int c0 = 0; c0 < D; c0 += kScoreSlab) {
-                __syncthreads();
+        for (int i = 0; i < 2; ++i) {
+            const int page = page0 + 8 * i;
+            const int phys = page < pages ? attn_page(a.table, a.max_pages, a.num_pages, b, page) : -1;
+            mean[i] = phys < 0 || !in_bounds(phys, a.num_pages) ? nullptr : a.mean + ((size_t)phys * a.Hkv + hk) * D + 4 * t;
+        }
+        unsigned long long best[2] = {0, 0};
+        for (int h0 = 0; h0 < a.group; h0 += 8) {
+            const int heads = min(8, a.group - h0);
+            float4 x[2][KB];
+            auto load = [&](int c0) {
 #pragma unroll
-                for (int i = tid; i < kScorePages * kScoreSlab / 4; i += kScoreThreads) {
-                    const int r = i / (kScoreSlab / 4), c = 4 * (i - r * (kScoreSlab / 4));
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (s_phys[r] >= 0)
-                        x = *reinterpret_cast<const float4*>(a.mean + ((size_t)s_phys[r] * a.Hkv + hk) * D + c0 + c);
-                    *reinterpret_cast<float4*>(&s_mean[r][c]) = x;
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int c = 0; c < KB; ++c) {
+                        x[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (mean[i] != nullptr) x[i][c] = *reinterpret_cast<const float4*>(mean[i] + c0 + 16 * c);
+                    }
+                }
+            };
+            load(0);
+            if (held != b * a.Hkv + hk || a.group > 8) {
+                __syncthreads();  // the queries before them have been read
+                for (int i = tid; i < D * 8; i += kScoreThreads) {
+                    const int h = i / D, c = i - h * D;
+                    // channel 16 m + 4 t + j of head h stands at step 4 m + j, lane 4 h + t
+                    s_q[c / 16 * 4 + (c & 3)][4 * h + (c >> 2 & 3)] =
+                        h < heads ? (double)ld1(a.q, BF ? kBF16 : kF16, ((size_t)b * a.Hq + hk * a.group + h0 + h) * D + c) : 0.0;
                 }
                 __syncthreads();
-#pragma unroll 2
-                for (int c = 0; c < kScoreSlab; c += 4) {
-                    const float4 x4 = *reinterpret_cast<const float4*>(&s_mean[tid][c]);
-                    const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+                held = b * a.Hkv + hk;
+            }
+            double sum[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const double xd = (double)x[e];
+            for (int c0 = 0; c0 < D; c0 += CH) {
+                if (c0 > 0) load(c0);
 #pragma unroll
-                        for (int h = 0; h < kScoreHeads; h += 2) {
-                            const double2 qd = *reinterpret_cast<const double2*>(&s_q[c0 + c + e][h]);
-                            sum[h] = fma(qd.x, xd, sum[h]);
-                            sum[h + 1] = fma(qd.y, xd, sum[h + 1]);
+                for (int c = 0; c < KB; ++c) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const double q = s_q[c0 / 4 + 4 * c + j][lane];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float4 v = x[i][c];
+                            dmma(sum[i], (double)(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w), q);
                         }
                     }
                 }
             }
+            // lane (g, t): page g, heads 2 t and 2 t + 1
 #pragma unroll
-            for (int h = 0; h < kScoreHeads; ++h) {
-                if (h < heads && sum[h] == sum[h]) {
-                    best = fmax(best, sum[h]);
-                    any = true;
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const unsigned long long key = 2 * t + e < heads ? sort_key(sum[i][e]) : 0ull;
+                    best[i] = key > best[i] ? key : best[i];
                 }
             }
         }
-        if (page < pages) {
-            const bool kept = page < a.n_first || page >= pages - a.n_last;
-            a.keys[((size_t)b * a.Hkv + hk) * a.max_pages + page] =
-                kept ? ~0ull : phys < 0 || !any ? 0ull : sort_key(best);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                const unsigned long long key = __shfl_xor_sync(0xffffffffu, best[i], o);
+                best[i] = key > best[i] ? key : best[i];
+            }
+            const int page = page0 + 8 * i;
+            if (t == 0 && page < pages)
+                a.keys[((size_t)b * a.Hkv + hk) * a.max_pages + page] = mean[i] == nullptr ? 0ull : best[i];
         }
     }
 }
@@ -222,39 +270,83 @@ __global__ void __launch_bounds__(kScoreThreads) attn_score_kernel(const AttnSel
 
 constexpr int kSelectThreads = 512;
 
-// Per (row, key head): the n_sel-th largest key by 8-bit digits from the top, each digit's counts in shared
-// memory (lanes with the same digit add once: the top digits of scores are nearly all alike), then the pages
-// above it, and the first ones equal to it, in page order.
+// Per (row, key head): the pages always kept, and of the others those with the largest keys.  The smallest key taken is
+// found by 8-bit digits, from the highest bit in which the keys differ, each digit's counts in shared memory; then come
+// the pages above it and the first ones equal to it, in page order.  The first 4096 pages' keys stay in registers.
+// Latency-bound: one CTA per list, three or four digits of two barriers each.
 __global__ void __launch_bounds__(kSelectThreads) attn_select_kernel(const AttnSelectArgs a) {
-    constexpr int WARPS = kSelectThreads / 32;
-    __shared__ int s_count[256], s_warp[WARPS], s_digit, s_need;
+    constexpr int WARPS = kSelectThreads / 32, C = 8, SPAN = C * kSelectThreads;
+    __shared__ __align__(16) int s_count[2][256];
+    __shared__ int s_part[C * WARPS], s_total, s_digit, s_need;
+    __shared__ unsigned s_bits[4];  // OR of the keys' words, and of their complements
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x / a.Hkv;
     const unsigned long long* keys = a.keys + (size_t)blockIdx.x * a.max_pages;
     int32_t* out = a.pages + (size_t)blockIdx.x * a.n_sel;
+    tc::wait_prerequisites();
+    tc::launch_dependents();
     const int len = attn_len(a.lens, b, (long long)a.max_pages * a.page_size);
     const int n = (len + a.page_size - 1) / a.page_size;
     if (n <= a.n_sel) {  // all of them
         for (int i = tid; i < a.n_sel; i += kSelectThreads) out[i] = i < n ? i : -1;
         return;
     }
-    unsigned long long prefix = 0, mask = 0;
-    int need = a.n_sel;  // of the keys that match the prefix
-    for (int shift = 56; shift >= 0; shift -= 8) {
-        if (tid < 256) s_count[tid] = 0;
-        __syncthreads();
-        for (int i0 = 0; i0 < n; i0 += kSelectThreads) {
-            const int i = i0 + tid;
-            const unsigned long long key = i < n ? keys[i] : 0;
-            const int digit = i < n && (key & mask) == prefix ? (int)(key >> shift & 255) : -1;
-            const unsigned same = __match_any_sync(0xffffffffu, digit);
-            if (digit >= 0 && lane == __ffs(same) - 1) atomicAdd(&s_count[digit], __popc(same));
+    auto kept = [&](int i) { return i < a.n_first || i >= n - a.n_last; };
+    unsigned long long reg[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int i = c * kSelectThreads + tid;
+        reg[c] = i < n && !kept(i) ? keys[i] : 0ull;
+    }
+    // f(page, key) for this thread's pages that are not kept
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int i = c * kSelectThreads + tid;
+            if (i < n && !kept(i)) f(i, reg[c]);
         }
+        for (int i = SPAN + tid; i < n; i += kSelectThreads)
+            if (!kept(i)) f(i, keys[i]);
+    };
+    const int need_all = a.n_sel - a.n_first - a.n_last;
+    if (tid < 4) s_bits[tid] = 0;
+    if (tid < 256) s_count[0][tid] = 0;
+    __syncthreads();
+    unsigned long long ones = 0, zeros = 0;
+    each([&](int, unsigned long long key) {
+        ones |= key;
+        zeros |= ~key;
+    });
+    const unsigned bits[4] = {__reduce_or_sync(0xffffffffu, (unsigned)(ones >> 32)), __reduce_or_sync(0xffffffffu, (unsigned)ones),
+                              __reduce_or_sync(0xffffffffu, (unsigned)(zeros >> 32)), __reduce_or_sync(0xffffffffu, (unsigned)zeros)};
+    if (lane < 4) {
+        const unsigned mine = lane == 0 ? bits[0] : lane == 1 ? bits[1] : lane == 2 ? bits[2] : bits[3];
+        atomicOr(&s_bits[lane], mine);
+    }
+    __syncthreads();
+    const unsigned long long differ =
+        ((unsigned long long)s_bits[0] << 32 | s_bits[1]) & ((unsigned long long)s_bits[2] << 32 | s_bits[3]);
+    // `mask`: the bits settled so far, `prefix`: their value in the smallest key taken, `need`: how many are still
+    // wanted of the keys that agree in them
+    int top = differ == 0 ? -1 : 63 - __clzll((long long)differ);
+    unsigned long long mask = top < 0 ? ~0ull : ~((2ull << top) - 1ull);  // top = 63: the shift gives 0, the mask 0
+    unsigned long long prefix = ((unsigned long long)s_bits[0] << 32 | s_bits[1]) & mask;
+    int need = need_all;
+    bool all = need == 0;
+    for (int turn = 0; top >= 0 && !all; ++turn) {
+        const int shift = top >= 7 ? top - 7 : 0, width = top - shift + 1;
+        int* count = s_count[turn & 1];
+        each([&](int, unsigned long long key) {
+            if ((key & mask) == prefix) atomicAdd(&count[(int)(key >> shift) & ((1 << width) - 1)], 1);
+        });
+        if (tid < 256) s_count[turn & 1 ^ 1][tid] = 0;
         __syncthreads();
         if (warp == 0) {  // lane l: digits 255 - 8 l down to 248 - 8 l
+            const int4 hi = reinterpret_cast<const int4*>(count)[63 - 2 * lane], lo = reinterpret_cast<const int4*>(count)[62 - 2 * lane];
+            const int v[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
             int sum = 0;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) sum += s_count[255 - 8 * lane - u];
+            for (int u = 0; u < 8; ++u) sum += v[u];
             int above = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -264,46 +356,82 @@ __global__ void __launch_bounds__(kSelectThreads) attn_select_kernel(const AttnS
             above -= sum;  // keys with a digit above this lane's
             if (above < need && need <= above + sum) {
                 int d = 255 - 8 * lane;
-                while (above + s_count[d] < need) above += s_count[d--];
-                s_digit = d;
-                s_need = need - above;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    if (above < need && need <= above + v[u]) {
+                        s_digit = d - u;
+                        s_need = need - above;
+                        s_total = v[u];
+                    }
+                    above += v[u];
+                }
             }
         }
         __syncthreads();
         need = s_need;
+        all = s_total == need;
         prefix |= (unsigned long long)s_digit << shift;
-        mask |= 255ull << shift;
-        const bool all = s_count[s_digit] == need;
-        __syncthreads();
-        if (all) break;
+        mask |= ((1ull << width) - 1ull) << shift;
+        top = shift - 1;
     }
+    // Place of each flagged page among the flagged ones of this span; the number of them.
+    auto ranks = [&](const bool (&flag)[C], int (&rank)[C]) -> int {
+        unsigned vote[C];
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            vote[c] = __ballot_sync(0xffffffffu, flag[c]);
+            if (lane == 0) s_part[c * WARPS + warp] = __popc(vote[c]);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            constexpr int E = C * WARPS / 32;
+            int v[E], sum = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                v[e] = sum;
+                sum += s_part[lane * E + e];
+            }
+            int incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) s_part[lane * E + e] = v[e] + incl - sum;
+            if (lane == 31) s_total = incl;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < C; ++c) rank[c] = s_part[c * WARPS + warp] + __popc(vote[c] & ((1u << lane) - 1u));
+        return s_total;
+    };
     int written = 0, ties = 0;
-    for (int i0 = 0; i0 < n; i0 += kSelectThreads) {
-        const int i = i0 + tid;
-        const unsigned long long key = i < n ? keys[i] & mask : 0;
-        const bool tie = i < n && key == prefix;
-        const unsigned tied = __ballot_sync(0xffffffffu, tie);
-        if (lane == 0) s_warp[warp] = __popc(tied);
-        __syncthreads();
-        int rank = ties + __popc(tied & ((1u << lane) - 1u));
+    for (int i0 = 0; i0 < n; i0 += SPAN) {
+        bool take[C], tie[C];
+        int rank[C];
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) rank += s_warp[w];
-            ties += s_warp[w];
+        for (int c = 0; c < C; ++c) {
+            const int i = i0 + c * kSelectThreads + tid;
+            const bool fixed = i < n && kept(i);
+            const unsigned long long key = i0 == 0 ? reg[c] : i < n ? keys[i] : 0ull;
+            tie[c] = i < n && !fixed && (key & mask) == prefix && need_all > 0;
+            take[c] = fixed || (i < n && need_all > 0 && (key & mask) > prefix) || (tie[c] && all);
         }
-        __syncthreads();
-        const bool take = i < n && (key > prefix || (tie && rank < need));
-        const unsigned taken = __ballot_sync(0xffffffffu, take);
-        if (lane == 0) s_warp[warp] = __popc(taken);
-        __syncthreads();
-        int to = written + __popc(taken & ((1u << lane) - 1u));
+        if (!all) {  // more equal keys than wanted: the first ones
+            const int found = ranks(tie, rank);
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) to += s_warp[w];
-            written += s_warp[w];
+            for (int c = 0; c < C; ++c) take[c] |= tie[c] && ties + rank[c] < need;
+            ties += found;
         }
-        if (take && in_bounds(to, a.n_sel)) out[to] = i;
-        __syncthreads();
+        const int found = ranks(take, rank);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int i = i0 + c * kSelectThreads + tid, to = written + rank[c];
+            if (take[c] && in_bounds(to, a.n_sel)) out[to] = i;
+        }
+        written += found;
     }
 }
 

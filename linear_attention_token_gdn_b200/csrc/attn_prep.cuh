@@ -14,12 +14,16 @@
 // both halves of the rotated part, so that both members of a pair are in one lane, the others two
 // adjacent chunks behind it.  Every access is then 16 bytes wide, and the only exchange between lanes
 // is the sum of squares.  A unit (one token, up to `hps` heads of one of the tensors) computes its
-// angles once for its heads.  Angles are reduced in fp64, in revolutions: a position of 2^20 leaves an
-// fp32 angle only a few bits behind the point, while position * inv_freq / (2 pi) minus its nearest
-// integer is exact in fp64 to 2^-33 of a revolution, and sincospif takes it from there in fp32.
+// angles once for its heads, and keeps U rows in flight: a row's registers are loaded again as soon as it
+// is unpacked.  Angles are reduced in fp64, in revolutions: a position of 2^20 leaves an fp32 angle
+// only a few bits behind the point, while position * inv_freq / (2 pi) minus its nearest integer is exact
+// in fp64 to 2^-32 of a revolution.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "out_gate.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdn {
 
@@ -32,7 +36,7 @@ struct AttnPrepArgs {
     float eps;
     const int32_t* positions;
     const double* inv_freq;
-    int rot, N, Hq, Hkv, hps, cq, ck;           // heads per unit; units per token of q, and of k (and of v)
+    int rot, N, Hq, Hkv, hps, cq, ck;           // heads per unit; units per token of q, and of k (with v)
     int out_dt;
     void *q_out, *k_out, *v_out;                // k_out, v_out: the cache when CACHE
     const int32_t *cu, *table;
@@ -52,23 +56,91 @@ __device__ __forceinline__ bool attn_chunks(int l, int rot, int& i0, int& j0) {
     return false;
 }
 
-// cos and sin of position * inv_freq for the lane's 8 pairs.
-__device__ __forceinline__ void attn_angles(const double* inv_freq, int i0, bool turns, int position, float (&c)[8],
-                                            float (&s)[8]) {
-    if (turns) {
+// cos and sin of 2 pi phase / 2^32, from the Taylor series about the nearest quarter turn: |x| <= pi / 4, where the
+// first terms left out are x^10 / 10! < 2^-25 of the cosine and x^11 / 11! < 2^-28 of the sine.
+__device__ __forceinline__ void attn_turn(int phase, float& c, float& s) {
+    const unsigned quarter = ((unsigned)phase + 0x20000000u) >> 30;
+    const float x = (float)(int)((unsigned)phase - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float x2 = x * x;
+    const float sx = fmaf(x * x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), x);
+    const float cx = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 40320, -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+    const float s0 = quarter & 1 ? cx : sx, c0 = quarter & 1 ? sx : cx;
+    s = __uint_as_float(__float_as_uint(s0) ^ (quarter << 30 & 0x80000000u));
+    c = __uint_as_float(__float_as_uint(c0) ^ ((quarter + 1) << 30 & 0x80000000u));
+}
+
+// The lane's 8 frequencies in revolutions per position (0 where it does not turn).
+__device__ __forceinline__ void attn_revs(const double* inv_freq, int i0, bool turns, double (&f)[8]) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            double rev = (double)position * (inv_freq[i0 + u] * 0.15915494309189533577);
-            rev -= rint(rev);
-            sincospif(2.0f * (float)rev, &s[u], &c[u]);
-        }
-    } else {
+    for (int u = 0; u < 8; u += 2) {
+        double2 v = make_double2(0.0, 0.0);
+        if (turns) v = *reinterpret_cast<const double2*>(inv_freq + i0 + u);
+        f[u] = v.x * 0.15915494309189533577;
+        f[u + 1] = v.y * 0.15915494309189533577;
+    }
+}
+
+// cos and sin of the lane's 8 angles.  Adding and taking away 1.5 * 2^52 rounds to whole revolutions, the fused
+// products leave the rest with one rounding, and adding 1.5 * 2^20 puts it, in units of 2^-32, into the low word: three
+// steps of the fp64 pipe and no conversion instruction, which run at a quarter of its rate and less.
+__device__ __forceinline__ void attn_angles(const double (&f)[8], int position, float (&c)[8], float (&s)[8]) {
+    const double p = (double)position;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            c[u] = 1.0f;
-            s[u] = 0.0f;
+    for (int u = 0; u < 8; ++u) {
+        const double whole = __dadd_rn(__fma_rn(p, f[u], 0x1.8p52), -0x1.8p52);
+        attn_turn(__double2loint(__dadd_rn(__fma_rn(p, f[u], -whole), 0x1.8p20)), c[u], s[u]);
+    }
+}
+
+// A lane's 16 channels of a row as they lie in memory.
+template <int IN>
+struct AttnRow {
+    static constexpr int Q = IN == kF32 ? 4 : 2;  // 16-byte words
+    uint4 w[Q];
+    __device__ __forceinline__ void load(const void* x, size_t row, int i0, int j0) {
+        using E = typename std::conditional<IN == kF32, uint32_t, uint16_t>::type;
+        const E* p = reinterpret_cast<const E*>(x) + row;
+#pragma unroll
+        for (int q = 0; q < Q / 2; ++q) {
+            w[q] = reinterpret_cast<const uint4*>(p + i0)[q];
+            w[Q / 2 + q] = reinterpret_cast<const uint4*>(p + j0)[q];
         }
     }
+    __device__ __forceinline__ void get(float (&xi)[8], float (&xj)[8]) const {
+        half(0, xi);
+        half(Q / 2, xj);
+    }
+
+  private:
+    __device__ __forceinline__ void half(int q0, float (&x)[8]) const {
+#pragma unroll
+        for (int q = 0; q < Q / 2; ++q) {
+            const uint32_t v[4] = {w[q0 + q].x, w[q0 + q].y, w[q0 + q].z, w[q0 + q].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (IN == kF32) {
+                    x[4 * q + e] = __uint_as_float(v[e]);
+                } else {
+                    const float2 f = unpack2<IN == kBF16>(v[e]);
+                    x[2 * e] = f.x;
+                    x[2 * e + 1] = f.y;
+                }
+            }
+        }
+    }
+};
+
+// The lanes of this lane's row.
+template <int LPR>
+__device__ __forceinline__ unsigned attn_row_mask() {
+    return (unsigned)((1ull << LPR) - 1) << (threadIdx.x & 31 & ~(LPR - 1));
+}
+
+template <int LPR>
+__device__ __forceinline__ float attn_row_sum(float x, unsigned mask) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+    return x;
 }
 
 __device__ __forceinline__ void attn_store8(void* p, int dt, size_t i, const float (&x)[8]) {
@@ -106,101 +178,101 @@ __device__ __forceinline__ int attn_seq_of(const int32_t* cu, int num_seqs, int 
 }
 
 template <int IN, int D, bool CACHE>
-__global__ void __launch_bounds__(kAttnPrepThreads) attn_prep_kernel(const AttnPrepArgs a) {
+__global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_prep_kernel(const AttnPrepArgs a) {
     constexpr int LPR = D / 16;                 // lanes of a row
     constexpr int U = IN == kF32 ? 2 : 4;       // rows in flight
     const int l = threadIdx.x % LPR;
-    const int per_token = a.cq + (CACHE ? 2 : 1) * a.ck;
+    const unsigned mask = attn_row_mask<LPR>();
+    // all tokens of the first heads, then of the next: a warp's rows then have one tensor and one number of heads
     const unsigned unit = (blockIdx.x * (unsigned)kAttnPrepThreads + threadIdx.x) / LPR;
-    int t = (int)(unit / (unsigned)per_token);
-    int c = (int)(unit - (unsigned)t * (unsigned)per_token);
-    bool live = t < a.N;
-    if (!live) t = 0;
-    const int part = c < a.cq ? 0 : c < a.cq + a.ck ? 1 : 2;  // q, k, v
-    const int heads = part == 0 ? a.Hq : a.Hkv;
-    const int h0 = (part == 0 ? c : part == 1 ? c - a.cq : c - a.cq - a.ck) * a.hps;
-    const void* x = part == 0 ? a.q : part == 1 ? a.k : a.v;
-    const size_t row0 = (size_t)t * (size_t)(part == 0 ? a.q_stride : part == 1 ? a.k_stride : a.v_stride);
-    const int position = a.positions[t];
-
-    void* out = part == 0 ? a.q_out : part == 1 ? a.k_out : a.v_out;
-    size_t dst0 = (size_t)t * heads * D, dst_step = D;  // of head 0, and from head to head
-    if constexpr (CACHE) {
-        if (position < 0) live = false;  // a padding token
-        if (live) {
-            const int seq = attn_seq_of(a.cu, a.num_seqs, a.N, t);
-            if (seq < 0) live = false;
-            else if (part > 0) {
-                const int page = position / a.page_size;
-                const int phys = attn_page(a.table, a.max_pages, a.num_pages, seq, page);
-                if (phys < 0) live = false;
-                else {
-                    dst0 = ((size_t)phys * a.Hkv * a.page_size + (position - page * a.page_size)) * D;
-                    dst_step = (size_t)a.page_size * D;
-                }
-            }
-        }
-    }
-
+    const int c = (int)(unit / (unsigned)a.N);
+    const int t = (int)(unit - (unsigned)c * (unsigned)a.N);
+    if (c >= a.cq + a.ck) return;
+    const bool keys = c >= a.cq;
+    const int heads = keys ? a.Hkv : a.Hq;
+    const int h0 = (keys ? c - a.cq : c) * a.hps;
+    const int n = min(a.hps, heads - h0);
+    const int rows = CACHE && keys ? 2 * n : n;  // keys, then the same heads' values
+    const void* x = keys ? a.k : a.q;
+    const size_t x0 = (size_t)t * (size_t)(keys ? a.k_stride : a.q_stride) + (size_t)h0 * D;
+    const size_t v0 = CACHE && keys ? (size_t)t * (size_t)a.v_stride + (size_t)h0 * D : 0;
     int i0, j0;
     const bool turns = attn_chunks(l, a.rot, i0, j0);
-    float cs[8], sn[8], wi[8], wj[8];
-    const float* w = part == 0 ? a.w_q : a.w_k;
-    attn_angles(a.inv_freq, i0, turns && part < 2, position, cs, sn);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        wi[u] = 1.0f + w[i0 + u];
-        wj[u] = 1.0f + w[j0 + u];
-    }
 
-    for (int hb = 0; hb < a.hps; hb += U) {
-        float xi[U][8], xj[U][8], ss[U];
+    AttnRow<IN> buf[U];
+    auto fetch = [&](AttnRow<IN>& to, int m) {
+        if (CACHE && m >= n) to.load(a.v, v0 + (size_t)(m - n) * D, i0, j0);
+        else to.load(x, x0 + (size_t)m * D, i0, j0);
+    };
+#pragma unroll
+    for (int m = 0; m < U; ++m) {
+        if (m < rows) fetch(buf[m], m);
+    }
+    const int position = a.positions[t];
+
+    size_t dst0 = ((size_t)t * heads + h0) * D, dst_step = D;  // of the first head, and from head to head
+    if constexpr (CACHE) {
+        if (position < 0) return;  // a padding token
+        const int seq = attn_seq_of(a.cu, a.num_seqs, a.N, t);
+        if (seq < 0) return;
+        if (keys) {
+            const int page = position / a.page_size;
+            const int phys = attn_page(a.table, a.max_pages, a.num_pages, seq, page);
+            if (phys < 0) return;
+            dst0 = (((size_t)phys * a.Hkv + h0) * a.page_size + (position - page * a.page_size)) * D;
+            dst_step = (size_t)a.page_size * D;
+        }
+    }
+    auto put = [&](void* out, int m, const float (&yi)[8], const float (&yj)[8]) {
+        const size_t o = dst0 + (size_t)m * dst_step;
+        if constexpr (CACHE) {
+            const long long cache = (long long)a.num_pages * a.Hkv * a.page_size * D;
+            if (!in_bounds((long long)(o + D - 1), keys ? cache : (long long)a.N * a.Hq * D)) return;
+        }
+        attn_store8(out, a.out_dt, o + i0, yi);
+        attn_store8(out, a.out_dt, o + j0, yj);
+    };
+
+    // y_i = r (x_i ci - x_j sj), y_j = r (x_j cj + x_i si), with 1 + w and the rotation in one factor each
+    float ci[8], cj[8], si[8], sj[8];
+    {
+        double f[8];
+        attn_revs(a.inv_freq, i0, turns, f);
+        attn_angles(f, position, ci, si);
+        const float* w = keys ? a.w_k : a.w_q;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const float wi = 1.0f + w[i0 + u], wj = 1.0f + w[j0 + u];
+            sj[u] = si[u] * wj;
+            cj[u] = ci[u] * wj;
+            si[u] *= wi;
+            ci[u] *= wi;
+        }
+    }
+    for (int hb = 0; hb < rows; hb += U) {
 #pragma unroll
         for (int m = 0; m < U; ++m) {
-            const int h = h0 + hb + m;
-            const bool ok = live && hb + m < a.hps && h < heads;
-            if (ok) {
-                ldv<IN, 8>(x, row0 + (size_t)h * D + i0, xi[m]);
-                ldv<IN, 8>(x, row0 + (size_t)h * D + j0, xj[m]);
-            } else {
-#pragma unroll
-                for (int u = 0; u < 8; ++u) xi[m][u] = xj[m][u] = 0.0f;
+            if (hb + m >= rows) break;
+            float xi[8], xj[8], ss = 0.0f, st = 0.0f;
+            buf[m].get(xi, xj);
+            if (hb + U + m < rows) fetch(buf[m], hb + U + m);
+            if (CACHE && hb + m >= n) {  // values go as they are
+                put(a.v_out, hb + m - n, xi, xj);
+                continue;
             }
-        }
-#pragma unroll
-        for (int m = 0; m < U; ++m) {
-            ss[m] = 0.0f;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) ss[m] = fmaf(xi[m][u], xi[m][u], fmaf(xj[m][u], xj[m][u], ss[m]));
-        }
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) {
-#pragma unroll
-            for (int m = 0; m < U; ++m) ss[m] += __shfl_xor_sync(0xffffffffu, ss[m], o);
-        }
-#pragma unroll
-        for (int m = 0; m < U; ++m) {
-            const int h = h0 + hb + m;
-            if (!(live && hb + m < a.hps && h < heads)) continue;
-            float yi[8], yj[8];
-            const float r = rsqrtf(ss[m] * (1.0f / D) + a.eps);
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const float ni = xi[m][u] * r * wi[u], nj = xj[m][u] * r * wj[u];
-                yi[u] = ni * cs[u] - nj * sn[u];
-                yj[u] = nj * cs[u] + ni * sn[u];
-                if (CACHE && part == 2) {  // values go as they are
-                    yi[u] = xi[m][u];
-                    yj[u] = xj[m][u];
-                }
+                ss = fmaf(xi[u], xi[u], ss);
+                st = fmaf(xj[u], xj[u], st);
             }
-            const size_t o = dst0 + (size_t)h * dst_step;
-            if constexpr (CACHE) {
-                const long long cache = (long long)a.num_pages * a.Hkv * a.page_size * D;
-                if (!in_bounds((long long)(o + D - 1), part == 0 ? (long long)a.N * a.Hq * D : cache)) continue;
+            const float r = rsqrtf(attn_row_sum<LPR>(ss + st, mask) * (1.0f / D) + a.eps);
+            float yi[8], yj[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                yi[u] = r * (xi[u] * ci[u] - xj[u] * sj[u]);
+                yj[u] = r * (xj[u] * cj[u] + xi[u] * si[u]);
             }
-            attn_store8(out, a.out_dt, o + i0, yi);
-            attn_store8(out, a.out_dt, o + j0, yj);
+            put(keys ? a.k_out : a.q_out, hb + m, yi, yj);
         }
     }
 }
@@ -216,22 +288,22 @@ struct AttnPrepBwdArgs {
     const double* inv_freq;
     int rot, N, Hq, Hkv, hps, cq, ck;
     int gq;                                     // blocks of the queries; the others take the keys
-    int dy_dt;
     void *dq, *dk;
     float* partial;                             // [blocks, d]: each block's share of dw
 };
 
-template <int IN, int D>
-__global__ void __launch_bounds__(kAttnPrepThreads) attn_prep_bwd_kernel(const AttnPrepBwdArgs a) {
+template <int IN, int D, int DY>
+__global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1 : 2)
+    attn_prep_bwd_kernel(const AttnPrepBwdArgs a) {
     constexpr int LPR = D / 16, SUBS = kAttnPrepThreads / LPR, WARPS = kAttnPrepThreads / 32;
     constexpr int U = IN == kF32 ? 1 : 2;
     __shared__ float s_dw[WARPS][D];
     const int l = threadIdx.x % LPR;
+    const unsigned mask = attn_row_mask<LPR>();
     const bool keys = (int)blockIdx.x >= a.gq;
     const int blk = keys ? blockIdx.x - a.gq : blockIdx.x;
     const int blocks = keys ? gridDim.x - a.gq : a.gq;
     const int heads = keys ? a.Hkv : a.Hq;
-    const int per_token = keys ? a.ck : a.cq;
     const void* x = keys ? a.k : a.q;
     const void* dy = keys ? a.dyk : a.dyq;
     void* dx = keys ? a.dk : a.dq;
@@ -248,80 +320,70 @@ __global__ void __launch_bounds__(kAttnPrepThreads) attn_prep_bwd_kernel(const A
         dwi[u] = dwj[u] = 0.0f;
     }
 
-    const long long units = (long long)a.N * per_token;  // < 2^31 (host check)
-    for (long long base = (long long)blk * SUBS; base < units; base += (long long)blocks * SUBS) {
-        const unsigned unit = (unsigned)base + threadIdx.x / LPR;
-        const bool live = unit < (unsigned)units;
-        const int t = live ? (int)(unit / (unsigned)per_token) : 0;
-        const int h0 = live ? (int)(unit - (unsigned)t * (unsigned)per_token) * a.hps : 0;
+    const unsigned units = (unsigned)a.N * (unsigned)(keys ? a.ck : a.cq);  // < 2^30 (host check)
+    for (unsigned unit = (unsigned)blk * SUBS + threadIdx.x / LPR; unit < units; unit += (unsigned)blocks * SUBS) {
+        const int c = (int)(unit / (unsigned)a.N), t = (int)(unit - (unsigned)c * (unsigned)a.N);
+        const int h0 = c * a.hps, n = min(a.hps, heads - h0);
+        const size_t x0 = (size_t)t * (size_t)stride + (size_t)h0 * D, g0 = ((size_t)t * heads + h0) * D;
+        AttnRow<IN> xb[U];
+        AttnRow<DY> gb[U];
+#pragma unroll
+        for (int m = 0; m < U; ++m) {
+            if (m < n) {
+                xb[m].load(x, x0 + (size_t)m * D, i0, j0);
+                gb[m].load(dy, g0 + (size_t)m * D, i0, j0);
+            }
+        }
         float cs[8], sn[8];
-        attn_angles(a.inv_freq, i0, turns, a.positions[t], cs, sn);
-        for (int hb = 0; hb < a.hps; hb += U) {
-            float xi[U][8], xj[U][8], gi[U][8], gj[U][8], ss[U], dot[U];
+        {
+            double f[8];
+            attn_revs(a.inv_freq, i0, turns, f);
+            attn_angles(f, a.positions[t], cs, sn);
+        }
+        for (int hb = 0; hb < n; hb += U) {
 #pragma unroll
             for (int m = 0; m < U; ++m) {
-                const int h = h0 + hb + m;
-                if (live && hb + m < a.hps && h < heads) {
-                    const size_t r = (size_t)t * (size_t)stride + (size_t)h * D, g = ((size_t)t * heads + h) * D;
-                    ldv<IN, 8>(x, r + i0, xi[m]);
-                    ldv<IN, 8>(x, r + j0, xj[m]);
-                    if (a.dy_dt == kF32) {
-                        ldv<kF32, 8>(dy, g + i0, gi[m]);
-                        ldv<kF32, 8>(dy, g + j0, gj[m]);
-                    } else if (a.dy_dt == kBF16) {
-                        ldv<kBF16, 8>(dy, g + i0, gi[m]);
-                        ldv<kBF16, 8>(dy, g + j0, gj[m]);
-                    } else {
-                        ldv<kF16, 8>(dy, g + i0, gi[m]);
-                        ldv<kF16, 8>(dy, g + j0, gj[m]);
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) xi[m][u] = xj[m][u] = gi[m][u] = gj[m][u] = 0.0f;
+                if (hb + m >= n) break;
+                float xi[8], xj[8], gi[8], gj[8];
+                xb[m].get(xi, xj);
+                gb[m].get(gi, gj);
+                if (hb + U + m < n) {
+                    xb[m].load(x, x0 + (size_t)(hb + U + m) * D, i0, j0);
+                    gb[m].load(dy, g0 + (size_t)(hb + U + m) * D, i0, j0);
                 }
-            }
-            // gi, gj become dn, and dot the sum of dn (1 + w) x
-#pragma unroll
-            for (int m = 0; m < U; ++m) {
-                ss[m] = dot[m] = 0.0f;
+                // gi, gj become dn, and dot the sum of dn (1 + w) x
+                float ss = 0.0f, dot = 0.0f;
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    const float ni = gi[m][u] * cs[u] + gj[m][u] * sn[u], nj = gj[m][u] * cs[u] - gi[m][u] * sn[u];
-                    gi[m][u] = ni;
-                    gj[m][u] = nj;
-                    ss[m] = fmaf(xi[m][u], xi[m][u], fmaf(xj[m][u], xj[m][u], ss[m]));
-                    dot[m] = fmaf(ni * wi[u], xi[m][u], fmaf(nj * wj[u], xj[m][u], dot[m]));
+                    const float ni = gi[u] * cs[u] + gj[u] * sn[u], nj = gj[u] * cs[u] - gi[u] * sn[u];
+                    gi[u] = ni;
+                    gj[u] = nj;
+                    ss = fmaf(xi[u], xi[u], fmaf(xj[u], xj[u], ss));
+                    dot = fmaf(ni * wi[u], xi[u], fmaf(nj * wj[u], xj[u], dot));
                 }
-            }
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) {
-#pragma unroll
-                for (int m = 0; m < U; ++m) {
-                    ss[m] += __shfl_xor_sync(0xffffffffu, ss[m], o);
-                    dot[m] += __shfl_xor_sync(0xffffffffu, dot[m], o);
+                for (int o = LPR / 2; o > 0; o >>= 1) {
+                    ss += __shfl_xor_sync(mask, ss, o);
+                    dot += __shfl_xor_sync(mask, dot, o);
                 }
-            }
-#pragma unroll
-            for (int m = 0; m < U; ++m) {
-                const int h = h0 + hb + m;
-                if (!(live && hb + m < a.hps && h < heads)) continue;
-                const float r = rsqrtf(ss[m] * (1.0f / D) + a.eps);
-                const float mean = dot[m] * r * (1.0f / D);  // mean of gn u
-                float yi[8], yj[8];
+                const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+                const float back = r * (r * (dot * r * (1.0f / D)));  // r^2 mean(gn u), of x
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    const float ui = xi[m][u] * r, uj = xj[m][u] * r;
-                    dwi[u] = fmaf(gi[m][u], ui, dwi[u]);
-                    dwj[u] = fmaf(gj[m][u], uj, dwj[u]);
-                    yi[u] = r * (gi[m][u] * wi[u] - ui * mean);
-                    yj[u] = r * (gj[m][u] * wj[u] - uj * mean);
+                    gi[u] *= r;
+                    gj[u] *= r;
+                    dwi[u] = fmaf(gi[u], xi[u], dwi[u]);
+                    dwj[u] = fmaf(gj[u], xj[u], dwj[u]);
+                    gi[u] = gi[u] * wi[u] - xi[u] * back;
+                    gj[u] = gj[u] * wj[u] - xj[u] * back;
                 }
-                const size_t g = ((size_t)t * heads + h) * D;
-                stv<IN, 8>(dx, g + i0, yi);
-                stv<IN, 8>(dx, g + j0, yj);
+                const size_t g = g0 + (size_t)(hb + m) * D;
+                stv<IN, 8>(dx, g + i0, gi);
+                stv<IN, 8>(dx, g + j0, gj);
             }
         }
     }
+    tc::launch_dependents();
 
     // this block's share of dw: lanes of the same channels, then the warps, in a fixed order
 #pragma unroll
@@ -348,25 +410,26 @@ __global__ void __launch_bounds__(kAttnPrepThreads) attn_prep_bwd_kernel(const A
     }
 }
 
-// dw_q, dw_k: the blocks' shares added in fp64, in block order within each of 8 strided sums.
-// Grid (2, ceil(d / 32)), block (32, 8).
-__global__ void __launch_bounds__(256) attn_prep_dw_kernel(const float* __restrict__ partial, int gq, int blocks, int d,
-                                                           float* __restrict__ dw_q, float* __restrict__ dw_k) {
-    __shared__ double s[8][32];
+// dw_q, dw_k: the blocks' shares added in fp64, in block order within each of 32 strided sums.
+// Grid (2, ceil(d / 32)), block (32, 32).
+__global__ void __launch_bounds__(1024) attn_prep_dw_kernel(const float* __restrict__ partial, int gq, int blocks, int d,
+                                                            float* __restrict__ dw_q, float* __restrict__ dw_k) {
+    __shared__ double s[32][33];
     const int i = blockIdx.y * 32 + threadIdx.x;
     const int b0 = blockIdx.x == 0 ? 0 : gq, b1 = blockIdx.x == 0 ? gq : blocks;
+    tc::wait_prerequisites();
     double sum = 0.0;
     if (i < d) {
 #pragma unroll 4
-        for (int b = b0 + threadIdx.y; b < b1; b += 8) sum += (double)partial[(size_t)b * d + i];
+        for (int b = b0 + threadIdx.y; b < b1; b += 32) sum += (double)partial[(size_t)b * d + i];
     }
     s[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
-    if (threadIdx.y == 0 && i < d) {
+    sum = s[threadIdx.x][threadIdx.y];
 #pragma unroll
-        for (int m = 1; m < 8; ++m) sum += s[m][threadIdx.x];
-        (blockIdx.x == 0 ? dw_q : dw_k)[i] = (float)sum;
-    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int j = blockIdx.y * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && j < d) (blockIdx.x == 0 ? dw_q : dw_k)[j] = (float)sum;
 }
 
 }  // namespace gdn
