@@ -144,7 +144,7 @@ bool attn_head_dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128 
 // ---------------------------------------------------------------- decode
 
 template <bool BF, int D, int NT, bool CHOSEN>
-gdn_status_t attn_decode_run(const gdn::AttnDecodeArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+gdn_status_t attn_decode_run(gdn::AttnDecodeArgs a, const DeviceInfo& dev, cudaStream_t st) {
     using S = gdn::AttnShape<D, NT>;
     static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
     static std::atomic<int> per_sm{0};
@@ -160,13 +160,17 @@ gdn_status_t attn_decode_run(const gdn::AttnDecodeArgs& a, const DeviceInfo& dev
     }
     int ctas = dev.sms * per_sm.load(std::memory_order_relaxed);
     if (ctas > gdn::kAttnMaxCtas) ctas = gdn::kAttnMaxCtas;
+    // few pairs: many pieces each, so one head per block and sixteen warps over its pieces, and a block per pair: one
+    // per CTA would be mostly blocks without a pair
+    const long long pairs = (long long)a.B * a.Hkv * a.hblocks;
+    a.by_pair = pairs * 4 < ctas;
     gdn_status_t r = launch_after("attn_decode_kernel", kernel, dim3((unsigned)ctas), dim3(gdn::kAttnThreads), S::SMEM, st, a);
     if (r != GDN_OK) return r;
-    // few work rows: many pieces each, so one head per block and eight warps over its pieces
-    const bool spread = (long long)a.B * a.Hkv * a.hblocks * 4 < ctas;
-    const int per = spread ? 1 : 8;
-    return launch_after("attn_join_kernel", gdn::attn_join_kernel<D, NT>, dim3((unsigned)ctas, (unsigned)(S::HB / per)), dim3(256),
-                        0, st, a, ctas, per);
+    if (a.by_pair)
+        return launch_after("attn_join_kernel", gdn::attn_join_kernel<D, NT, 16>, dim3((unsigned)pairs, (unsigned)S::HB), dim3(512),
+                            0, st, a, ctas, 1);
+    return launch_after("attn_join_kernel", gdn::attn_join_kernel<D, NT, 8>, dim3((unsigned)ctas, (unsigned)NT), dim3(256), 0, st, a,
+                        ctas, 8);
 }
 
 template <bool BF, int D>
@@ -362,12 +366,17 @@ gdn_status_t gdn_attn_prep_bwd(const void* dq_out, const void* dk_out, const voi
     bk = bk < 1 ? 1 : bk;
     if (bq > (uq + subs - 1) / subs) bq = (uq + subs - 1) / subs;
     if (bk > (uk + subs - 1) / subs) bk = (uk + subs - 1) / subs;
+    // one block of each (it has at most two units per lane group): it writes dw itself
+    const bool direct = uq <= 2 * subs && uk <= 2 * subs;
+    if (direct) bq = bk = 1;
     a.gq = (int)bq;
+    a.dw_q = direct ? dw_q : nullptr;
+    a.dw_k = dw_k;
     const unsigned blocks = (unsigned)(bq + bk);
     if (in_dtype == GDN_F32) r = attn_prep_bwd_dy<gdn::kF32>(d, (int)dy_dtype, a, blocks, st);
     else if (in_dtype == GDN_BF16) r = attn_prep_bwd_dy<gdn::kBF16>(d, (int)dy_dtype, a, blocks, st);
     else r = attn_prep_bwd_dy<gdn::kF16>(d, (int)dy_dtype, a, blocks, st);
-    if (r != GDN_OK) return r;
+    if (r != GDN_OK || direct) return r;
     return launch_after("attn_prep_dw_kernel", gdn::attn_prep_dw_kernel, dim3(2, (unsigned)((d + 31) / 32)), dim3(32, 32), 0, st,
                         (const float*)a.partial, a.gq, (int)blocks, d, dw_q, dw_k);
 }
@@ -437,7 +446,8 @@ gdn_status_t gdn_attn_page_mean(const void* k_cache, const int32_t* page_table, 
     a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages; a.mean = page_mean;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const long long most = (long long)B * Hkv * max_pages;  // units at most
-    const unsigned grid = (unsigned)(most < 8LL * dev.sms ? most : 8LL * dev.sms);
+    const long long room = (long long)gdn::kMeanPerSm * dev.sms;
+    const unsigned grid = (unsigned)(most < room ? most : room);
     return dtype == GDN_BF16 ? attn_mean_launch<true>(d, a, grid, st) : attn_mean_launch<false>(d, a, grid, st);
 }
 
@@ -474,7 +484,8 @@ gdn_status_t gdn_attn_select(const void* q, const float* page_mean, const int32_
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (max_pages > n_sel) {  // else every row has all its pages chosen
         const long long most = (long long)B * Hkv * ((max_pages + gdn::kScorePages - 1) / gdn::kScorePages);
-        const unsigned grid = (unsigned)(most < 4LL * dev.sms ? most : 4LL * dev.sms);
+        const long long room = (long long)gdn::attn_score_per_sm(d) * dev.sms;
+        const unsigned grid = (unsigned)(most < room ? most : room);
         r = dtype == GDN_BF16 ? attn_score_launch<true>(d, a, grid, st) : attn_score_launch<false>(d, a, grid, st);
         if (r != GDN_OK) return r;
     }

@@ -118,8 +118,11 @@ struct AttnDecodeArgs {
     float scale_log2;                           // scale * log2(e)
     int y_dt;
     void* y;
-    int* meta;                                  // [grid][2]: the pair whose first piece this CTA holds (-1: none), and
-                                                // the number of its pieces, one per CTA from here on
+    // meta, where a piece is a CTA's part of a pair, a pair a (row, key head, head block), and a pair's pieces are in
+    // CTAs that follow one another.  by_pair: [pair][2], the CTA of the first piece and the number of pieces (1 or 0: no
+    // join).  Otherwise [CTA][2], the pair whose first piece the CTA holds (-1: none, or the only one) and their number.
+    int* meta;
+    int by_pair;
     float* part;                                // [grid][2][8 NT][D + 2]: o, then m and l (log2 scale)
 };
 
@@ -183,8 +186,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
 
     // rows without a key
     for (int b = cta; b < a.B; b += gridDim.x) {
-        if (a.lens[b] <= 0)
+        if (a.lens[b] <= 0) {
             for (int i = tid; i < a.Hq * D; i += kAttnThreads) st1(a.y, a.y_dt, (size_t)b * a.Hq * D + i, 0.0f);
+            if (a.by_pair)
+                for (int i = tid; i < pairs; i += kAttnThreads) a.meta[2 * (b * pairs + i) + 1] = 0;
+        }
     }
 
     long long share = 0;
@@ -408,9 +414,16 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
         }
         __syncthreads();
         const bool whole = first == 0 && last == tiles;
-        if (!whole && first == 0) {
-            starting = (b * a.Hkv + hk) * a.hblocks + hb;
-            pieces = (int)((row_base + (long long)(pair + 1) * tiles - 1) / share) - cta + 1;
+        if (first == 0) {
+            const int last_cta = (int)((row_base + (long long)(pair + 1) * tiles - 1) / share);
+            if (!whole) {
+                starting = b * pairs + pair;
+                pieces = last_cta - cta + 1;
+            }
+            if (a.by_pair && tid == 0) {
+                a.meta[2 * (b * pairs + pair)] = cta;
+                a.meta[2 * (b * pairs + pair) + 1] = last_cta - cta + 1;
+            }
         }
         float* piece = a.part + ((size_t)cta * 2 + (first == 0 ? 1 : 0)) * S::PIECE;
         for (int i = tid; i < heads * (D / 2); i += kAttnThreads) {
@@ -440,35 +453,38 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
         }
         at += last - first;
     }
-    if (tid == 0) {
+    if (!a.by_pair && tid == 0) {
         a.meta[2 * cta] = starting;
         a.meta[2 * cta + 1] = pieces;
     }
 }
 
 // Joins the pieces of a (row, key head, head block) that several CTAs share: y = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
-// M = max m_i.  CTA x looks at the pair whose first piece CTA x of the first kernel held, blockIdx.y at `per` heads of
-// it, with 8 / per warps a head, each taking every (8 / per)-th piece.  M and the weights' sum come first, from all pieces
+// M = max m_i.  CTA x takes pair x (by_pair), or the pair whose first piece CTA x of the first kernel held, blockIdx.y at `per` heads of
+// it, with W / per warps a head, each taking every (W / per)-th piece.  M and the weights' sum come first, from all pieces
 // at once, so that the loads of the o_i do not wait for one another.
-template <int D, int NT>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnDecodeArgs a, int ctas, int per) {
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(32 * W) attn_join_kernel(const AttnDecodeArgs a, int ctas, int per) {
     using S = AttnShape<D, NT>;
     constexpr int E = D / 32, V = E < 4 ? E : 4;  // channels of a lane, of one load
-    __shared__ float s_o[8][D];
+    __shared__ float s_o[W][D];
     tc::wait_prerequisites();
-    const int row = a.meta[2 * blockIdx.x], pieces = min(a.meta[2 * blockIdx.x + 1], ctas - (int)blockIdx.x);
-    if (row < 0) return;
+    const int held = a.meta[2 * blockIdx.x], pieces = a.meta[2 * blockIdx.x + 1];
+    const int row = a.by_pair ? blockIdx.x : held, cta0 = a.by_pair ? held : blockIdx.x;
+    if (a.by_pair ? pieces <= 1 : row < 0) return;
+    if (!in_bounds(cta0 + pieces - 1, ctas)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int hb = row % a.hblocks, hk = row / a.hblocks % a.Hkv, b = row / a.hblocks / a.Hkv;
     const int heads = min(S::HB, a.group - hb * S::HB);
-    const int strides = 8 / per;
+    const int strides = W / per;
     const int h = blockIdx.y * per + warp % per, sub = warp / per;
     const bool live = h < heads;
-    auto piece = [&](int i) { return a.part + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * S::PIECE; };
+    auto piece = [&](int i) { return a.part + ((size_t)(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * S::PIECE; };
     float top = -INFINITY, sum = 0.0f, y[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) y[e] = 0.0f;
     if (live) {
+#pragma unroll 4
         for (int i = lane; i < pieces; i += 32) {
             const float2 ml = *reinterpret_cast<const float2*>(piece(i) + S::HB * D + 2 * h);
             const float next = fmaxf(top, ml.x);
@@ -501,7 +517,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnDecodeArgs a, 
         for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = y[e];
         __syncthreads();
         if (sub == 0) {
-            for (int w = per + warp; w < 8; w += per) {
+            for (int w = per + warp; w < W; w += per) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[e] += s_o[w][lane + 32 * e];
             }

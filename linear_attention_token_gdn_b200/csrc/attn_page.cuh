@@ -15,7 +15,7 @@ namespace gdn {
 
 // ---------------------------------------------------------------- mean keys
 
-constexpr int kMeanThreads = 128;
+constexpr int kMeanThreads = 128, kMeanPerSm = 7;  // CTAs an SM: the grid is one resident wave
 
 struct AttnMeanArgs {
     const void* k_cache;
@@ -39,7 +39,7 @@ __device__ __forceinline__ int attn_touched(const AttnMeanArgs& a, int b, int& f
 // this one's sums are joined over the CTA, and its place in the cache is looked up one page earlier still, so memory
 // never waits for the join.  Sums are fp32, in a fixed order.
 template <bool BF, int D>
-__global__ void __launch_bounds__(kMeanThreads) attn_page_mean_kernel(const AttnMeanArgs a) {
+__global__ void __launch_bounds__(kMeanThreads, kMeanPerSm) attn_page_mean_kernel(const AttnMeanArgs a) {
     constexpr int LPR = D / 8, RPP = kMeanThreads / LPR, U = 8;  // lanes of a key, keys of a pass, passes in flight
     __shared__ __align__(16) float s_sum[2][RPP][D];  // written 16 bytes at a time
     const int tid = threadIdx.x, l = tid % LPR, sub = tid / LPR;
@@ -55,32 +55,42 @@ __global__ void __launch_bounds__(kMeanThreads) attn_page_mean_kernel(const Attn
             share = (total + gridDim.x - 1) / gridDim.x;
             return share * blockIdx.x;
         });
-    const long long end = min(share * blockIdx.x + share, place.total);
-    int b = place.b, first = 0, n = 0;
-    long long row_base = place.before;
-    if (share * blockIdx.x < end) n = attn_touched(a, b, first);
-    // Item `at` of the line: its (page, key head) in the cache, or -1, and its keys inside the row.
+    long long at = share * blockIdx.x;
+    const long long end = min(at + share, place.total);
+    // the walk along the line: row b, its page `first + i`, key head hk; a row's pages outside, its key heads inside
+    int b = place.b, first = 0, n = 0, i = 0, hk = 0, len = 0;
+    if (at < end) {
+        n = attn_touched(a, b, first);
+        len = a.lens[b];
+        i = (int)((at - place.before) / a.Hkv);
+        hk = (int)(at - place.before - (long long)i * a.Hkv);
+    }
+    // Next item of the line: its (page, key head) in the cache, or -1, and its keys inside the row.
     struct Item {
         long long slot;
         int count;
     };
-    auto find = [&](long long at) -> Item {
+    auto find = [&](bool more) -> Item {
         Item it{-1, 0};
-        if (at >= end) return it;
-        while (at >= row_base + (long long)n * a.Hkv) {
-            row_base += (long long)n * a.Hkv;
+        if (!more) return it;
+        while (i == n) {
             n = attn_touched(a, ++b, first);
+            len = a.lens[b];
+            i = 0;
         }
-        const int i = (int)((at - row_base) / a.Hkv), hk = (int)(at - row_base - (long long)i * a.Hkv);
         const int page = first + i;
-        it.count = min(a.page_size, a.lens[b] - page * a.page_size);
+        it.count = min(a.page_size, len - page * a.page_size);
         const int phys = a.table[(size_t)b * a.max_pages + page];
         if (phys < 0 || phys >= a.num_pages || it.count <= 0) {  // uniform
             if (tid == 0) raise_error(kErrPage);
-            return it;
+        } else {
+            it.slot = (long long)phys * a.Hkv + hk;
+            if (!in_bounds(it.slot, (long long)a.num_pages * a.Hkv)) it.slot = -1;
         }
-        it.slot = (long long)phys * a.Hkv + hk;
-        if (!in_bounds(it.slot, (long long)a.num_pages * a.Hkv)) it.slot = -1;
+        if (++hk == a.Hkv) {
+            hk = 0;
+            ++i;
+        }
         return it;
     };
     uint4 x[U];
@@ -94,8 +104,7 @@ __global__ void __launch_bounds__(kMeanThreads) attn_page_mean_kernel(const Attn
         }
     };
 
-    long long at = share * blockIdx.x;
-    Item now = find(at), next = find(at + 1);
+    Item now = find(at < end), next = find(at + 1 < end);
     load(now, sub);
     int parity = 0;
     for (; at < end; ++at) {
@@ -118,7 +127,7 @@ __global__ void __launch_bounds__(kMeanThreads) attn_page_mean_kernel(const Attn
         const Item done = now;
         now = next;
         load(now, sub);
-        next = find(at + 2);
+        next = find(at + 2 < end);
         if (done.slot < 0) continue;  // uniform
         stv<kF32, 8>(s_sum[parity][sub], 8 * l, sum);
         __syncthreads();  // the other buffer's readers have passed the sync before
@@ -143,7 +152,10 @@ struct AttnSelectArgs {
     int32_t* pages;                             // [B, Hkv, n_sel]
 };
 
-constexpr int kScoreThreads = 128, kScorePages = 16 * kScoreThreads / 32;  // 16 pages a warp
+constexpr int kScoreThreads = 128, kScorePages = 8 * kScoreThreads / 32;  // 8 pages a warp
+
+// CTAs an SM, by the registers that two pages' loads take: the grid is one resident wave.
+__host__ __device__ constexpr int attn_score_per_sm(int d) { return d == 256 ? 2 : d == 128 ? 4 : 5; }
 
 // A double as an unsigned number of the same order; NaN is the lowest.
 __device__ __forceinline__ unsigned long long sort_key(double x) {
@@ -158,14 +170,15 @@ __device__ __forceinline__ void dmma(double (&c)[2], double a, double b) {
                  : "d"(a), "d"(b));
 }
 
-// Scores of 64 pages of a (row, key head) at a time, 16 per warp in two 8 x 8 x 4 fp64 products, whose 8 columns are
+// Scores of 32 pages of a (row, key head) at a time, 8 per warp in 8 x 8 x 4 fp64 products, whose 8 columns are
 // query heads.  The contraction runs over channels in any order, so a lane's 4 channels of a page are one 16-byte load,
 // all of a page's loads (8 at d = 128) are in flight together, and nothing of the means goes through shared memory;
-// only the queries do, as doubles in fragment order, once per (row, key head).  Bound by HBM (the means) and by the
-// conversions to fp64, 16 a clock and SM: 4 us and 10 us of the 64-row case's 16800 pages of 8 key heads.
+// only the queries do, as doubles in fragment order, once per (row, key head).  The next pages' means load under this
+// one's products, their places in the cache having been looked up one step earlier; four independent sums keep a step's
+// products from waiting for one another.  What bounds it: HBM (the means) and the conversions to fp64, 16 a clock and SM.
 template <bool BF, int D>
-__global__ void __launch_bounds__(kScoreThreads) attn_score_kernel(const AttnSelectArgs a) {
-    constexpr int CH = D < 128 ? D : 128, KB = CH / 16;  // channels in flight, 16-byte loads of a page for them
+__global__ void __launch_bounds__(kScoreThreads, attn_score_per_sm(D)) attn_score_kernel(const AttnSelectArgs a) {
+    constexpr int KB = D / 16;  // 16-byte loads of a page
     __shared__ double s_q[D / 4][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     tc::wait_prerequisites();
@@ -182,100 +195,112 @@ __global__ void __launch_bounds__(kScoreThreads) attn_score_kernel(const AttnSel
         });
     long long at = share * blockIdx.x;
     const long long end = min(at + share, place.total);
-    int b = place.b, pages = 0, n = 0, held = -1;  // held: the (row, key head) whose queries are in s_q
-    long long row_base = place.before;
-    if (at < end) n = blocks_of(pages = pages_of(b));
-    for (; at < end; ++at) {
-        while (at >= row_base + (long long)n * a.Hkv) {
-            row_base += (long long)n * a.Hkv;
+    // the walk along the line: row b, key head hk, block blk of its pages; key heads outside, blocks inside
+    int b = place.b, pages = 0, n = 0, hk = 0, blk = 0;
+    if (at < end) {
+        n = blocks_of(pages = pages_of(b));
+        hk = (int)((at - place.before) / n);
+        blk = (int)(at - place.before - (long long)hk * n);
+    }
+    struct Item {
+        int b, hk, page, phys;  // this lane's page (-1: behind the row's last) and its place in the cache (-1: none)
+    };
+    auto find = [&](bool more) -> Item {
+        Item it{0, 0, -1, -1};
+        if (!more) return it;
+        while (hk == a.Hkv || n == 0) {
             n = blocks_of(pages = pages_of(++b));
+            hk = 0;
         }
-        const int hk = (int)((at - row_base) / n);
-        const int page0 = (int)(at - row_base - (long long)hk * n) * kScorePages + warp * 16 + g;
-        const float* mean[2];
+        it.b = b;
+        it.hk = hk;
+        const int page = blk * kScorePages + warp * 8 + g;
+        if (page < pages) {
+            it.page = page;
+            it.phys = attn_page(a.table, a.max_pages, a.num_pages, b, page);
+            if (it.phys >= 0 && !in_bounds(it.phys, a.num_pages)) it.phys = -1;
+        }
+        if (++blk == n) {
+            blk = 0;
+            ++hk;
+        }
+        return it;
+    };
+    float4 x[KB];
+    auto load = [&](const Item& it) {
+        const float* mean = a.mean + ((size_t)it.phys * a.Hkv + it.hk) * D + 4 * t;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int page = page0 + 8 * i;
-            const int phys = page < pages ? attn_page(a.table, a.max_pages, a.num_pages, b, page) : -1;
-            mean[i] = phys < 0 || !in_bounds(phys, a.num_pages) ? nullptr : a.mean + ((size_t)phys * a.Hkv + hk) * D + 4 * t;
+        for (int c = 0; c < KB; ++c) {
+            x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (it.phys >= 0) x[c] = *reinterpret_cast<const float4*>(mean + 16 * c);
         }
-        unsigned long long best[2] = {0, 0};
+    };
+
+    Item now = find(at < end), next = find(at + 1 < end);
+    load(now);
+    int held = -1;  // the (row, key head) whose queries are in s_q
+    for (; at < end; ++at) {
+        float4 m[KB];
+#pragma unroll
+        for (int c = 0; c < KB; ++c) m[c] = x[c];
+        const Item item = now;
+        now = next;
+        load(now);
+        next = find(at + 2 < end);
+        unsigned long long best = 0;
         for (int h0 = 0; h0 < a.group; h0 += 8) {
             const int heads = min(8, a.group - h0);
-            float4 x[2][KB];
-            auto load = [&](int c0) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                    for (int c = 0; c < KB; ++c) {
-                        x[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (mean[i] != nullptr) x[i][c] = *reinterpret_cast<const float4*>(mean[i] + c0 + 16 * c);
-                    }
-                }
-            };
-            load(0);
-            if (held != b * a.Hkv + hk || a.group > 8) {
+            if (held != item.b * a.Hkv + item.hk || a.group > 8) {
                 __syncthreads();  // the queries before them have been read
                 for (int i = tid; i < D * 8; i += kScoreThreads) {
                     const int h = i / D, c = i - h * D;
                     // channel 16 m + 4 t + j of head h stands at step 4 m + j, lane 4 h + t
                     s_q[c / 16 * 4 + (c & 3)][4 * h + (c >> 2 & 3)] =
-                        h < heads ? (double)ld1(a.q, BF ? kBF16 : kF16, ((size_t)b * a.Hq + hk * a.group + h0 + h) * D + c) : 0.0;
+                        h < heads ? (double)ld1(a.q, BF ? kBF16 : kF16, ((size_t)item.b * a.Hq + item.hk * a.group + h0 + h) * D + c)
+                                  : 0.0;
                 }
                 __syncthreads();
-                held = b * a.Hkv + hk;
+                held = item.b * a.Hkv + item.hk;
             }
-            double sum[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
+            double sum[4][2];
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += CH) {
-                if (c0 > 0) load(c0);
+            for (int j = 0; j < 4; ++j) sum[j][0] = sum[j][1] = 0.0;
 #pragma unroll
-                for (int c = 0; c < KB; ++c) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const double q = s_q[c0 / 4 + 4 * c + j][lane];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float4 v = x[i][c];
-                            dmma(sum[i], (double)(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w), q);
-                        }
-                    }
-                }
+            for (int c = 0; c < KB; ++c) {
+                dmma(sum[0], (double)m[c].x, s_q[4 * c][lane]);
+                dmma(sum[1], (double)m[c].y, s_q[4 * c + 1][lane]);
+                dmma(sum[2], (double)m[c].z, s_q[4 * c + 2][lane]);
+                dmma(sum[3], (double)m[c].w, s_q[4 * c + 3][lane]);
             }
             // lane (g, t): page g, heads 2 t and 2 t + 1
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const unsigned long long key = 2 * t + e < heads ? sort_key(sum[i][e]) : 0ull;
-                    best[i] = key > best[i] ? key : best[i];
-                }
+            for (int e = 0; e < 2; ++e) {
+                const double score = (sum[0][e] + sum[1][e]) + (sum[2][e] + sum[3][e]);
+                const unsigned long long key = 2 * t + e < heads ? sort_key(score) : 0ull;
+                best = key > best ? key : best;
             }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                const unsigned long long key = __shfl_xor_sync(0xffffffffu, best[i], o);
-                best[i] = key > best[i] ? key : best[i];
-            }
-            const int page = page0 + 8 * i;
-            if (t == 0 && page < pages)
-                a.keys[((size_t)b * a.Hkv + hk) * a.max_pages + page] = mean[i] == nullptr ? 0ull : best[i];
+        for (int o = 1; o < 4; o <<= 1) {
+            const unsigned long long key = __shfl_xor_sync(0xffffffffu, best, o);
+            best = key > best ? key : best;
         }
+        if (t == 0 && item.page >= 0)
+            a.keys[((size_t)item.b * a.Hkv + item.hk) * a.max_pages + item.page] = item.phys < 0 ? 0ull : best;
     }
 }
 
 // ---------------------------------------------------------------- choice
 
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 256;
 
 // Per (row, key head): the pages always kept, and of the others those with the largest keys.  The smallest key taken is
 // found by 8-bit digits, from the highest bit in which the keys differ, each digit's counts in shared memory; then come
-// the pages above it and the first ones equal to it, in page order.  The first 4096 pages' keys stay in registers.
+// the pages above it and the first ones equal to it, in page order.  The first 2048 pages' keys stay in registers.
 // Latency-bound: one CTA per list, three or four digits of two barriers each.
 __global__ void __launch_bounds__(kSelectThreads) attn_select_kernel(const AttnSelectArgs a) {
     constexpr int WARPS = kSelectThreads / 32, C = 8, SPAN = C * kSelectThreads;
+    static_assert(kSelectThreads == 256, "one thread per digit");
     __shared__ __align__(16) int s_count[2][256];
     __shared__ int s_part[C * WARPS], s_total, s_digit, s_need;
     __shared__ unsigned s_bits[4];  // OR of the keys' words, and of their complements
@@ -303,6 +328,7 @@ __global__ void __launch_bounds__(kSelectThreads) attn_select_kernel(const AttnS
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = c * kSelectThreads + tid;
+            if (c * kSelectThreads >= n) break;
             if (i < n && !kept(i)) f(i, reg[c]);
         }
         for (int i = SPAN + tid; i < n; i += kSelectThreads)
@@ -310,7 +336,7 @@ __global__ void __launch_bounds__(kSelectThreads) attn_select_kernel(const AttnS
     };
     const int need_all = a.n_sel - a.n_first - a.n_last;
     if (tid < 4) s_bits[tid] = 0;
-    if (tid < 256) s_count[0][tid] = 0;
+    s_count[0][tid] = 0;
     __syncthreads();
     unsigned long long ones = 0, zeros = 0;
     each([&](int, unsigned long long key) {
@@ -339,7 +365,7 @@ __global__ void __launch_bounds__(kSelectThreads) attn_select_kernel(const AttnS
         each([&](int, unsigned long long key) {
             if ((key & mask) == prefix) atomicAdd(&count[(int)(key >> shift) & ((1 << width) - 1)], 1);
         });
-        if (tid < 256) s_count[turn & 1 ^ 1][tid] = 0;
+        s_count[(turn & 1) ^ 1][tid] = 0;
         __syncthreads();
         if (warp == 0) {  // lane l: digits 255 - 8 l down to 248 - 8 l
             const int4 hi = reinterpret_cast<const int4*>(count)[63 - 2 * lane], lo = reinterpret_cast<const int4*>(count)[62 - 2 * lane];

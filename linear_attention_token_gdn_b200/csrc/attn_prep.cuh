@@ -290,6 +290,7 @@ struct AttnPrepBwdArgs {
     int gq;                                     // blocks of the queries; the others take the keys
     void *dq, *dk;
     float* partial;                             // [blocks, d]: each block's share of dw
+    float *dw_q, *dw_k;                         // written by the only block of each tensor; dw_q NULL: shares
 };
 
 template <int IN, int D, int DY>
@@ -406,7 +407,8 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1
         float sum = 0.0f;
 #pragma unroll
         for (int m = 0; m < WARPS; ++m) sum += s_dw[m][i];
-        a.partial[(size_t)blockIdx.x * D + i] = sum;
+        if (a.dw_q != nullptr) (keys ? a.dw_k : a.dw_q)[i] = sum;
+        else a.partial[(size_t)blockIdx.x * D + i] = sum;
     }
 }
 

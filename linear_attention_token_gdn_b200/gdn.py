@@ -408,18 +408,18 @@ def _on_stream(fn):
     stream, so that what it allocates and launches belongs to that stream."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kwargs):
-        device = first.device
-        if device.type != "cuda":
+        if not first.is_cuda:
             raise ValueError("libgdn takes device tensors only")
-        if stream is None and device.index == torch.cuda.current_device():
+        if stream is None and first.get_device() == torch.cuda.current_device():
             return fn(first, *args, **kwargs)
-        with torch.cuda.device(device), torch.cuda.stream(stream):
+        with torch.cuda.device(first.device), torch.cuda.stream(stream):
             return fn(first, *args, **kwargs)
     return call
 
 
-def _now():
-    return torch.cuda.current_stream().cuda_stream
+def _now(device):
+    """Handle of the device's current stream (without the Stream object, which costs 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _arg(name, t, device, dtype, shape):
@@ -479,7 +479,7 @@ def attn_prep(q, k, w_q, w_k, positions, inv_freq, eps=1e-6, out_dtype=None, out
                                _arg("w_k", w_k, dev, torch.float32, (d,)), eps,
                                _arg("positions", positions, dev, torch.int32, (N,)), fp, rot, N, Hq, Hkv, d, _dt(q),
                                _dt(q_out), _arg("q_out", q_out, dev, q_out.dtype, (N, Hq, d)),
-                               _arg("k_out", k_out, dev, q_out.dtype, (N, Hkv, d)), _now()))
+                               _arg("k_out", k_out, dev, q_out.dtype, (N, Hkv, d)), _now(dev)))
     return q_out, k_out
 
 
@@ -507,7 +507,7 @@ def attn_prep_cache(q, k, v, w_q, w_k, positions, inv_freq, k_cache, v_cache, pa
         None if cu_seqlens is None else _arg("cu_seqlens", cu_seqlens, dev, torch.int32, (num_seqs + 1,)), num_seqs, N, Hq,
         Hkv, d, _arg("page_table", page_table, dev, torch.int32, (num_seqs, max_pages)), max_pages, num_pages, page_size,
         _dt(q), _dt(k_cache), _arg("q_out", q_out, dev, dtype, (N, Hq, d)), _arg("k_cache", k_cache, dev, dtype, cache),
-        _arg("v_cache", v_cache, dev, dtype, cache), _now()))
+        _arg("v_cache", v_cache, dev, dtype, cache), _now(dev)))
     return q_out
 
 
@@ -530,7 +530,7 @@ def attn_prep_bwd(dq_out, dk_out, q, k, w_q, w_k, positions, inv_freq, eps=1e-6,
         _arg("positions", positions, dev, torch.int32, (N,)), fp, rot, N, Hq, Hkv, d, _dt(q), _dt(dq_out),
         _arg("dq", out["dq"], dev, q.dtype, (N, Hq, d)), _arg("dk", out["dk"], dev, q.dtype, (N, Hkv, d)),
         _arg("dw_q", out["dw_q"], dev, torch.float32, (d,)), _arg("dw_k", out["dw_k"], dev, torch.float32, (d,)),
-        workspace.data_ptr(), _size(workspace), _now()))
+        workspace.data_ptr(), _size(workspace), _now(dev)))
     return out
 
 
@@ -551,7 +551,7 @@ def attn_decode(q, k_cache, v_cache, page_table, lens, pages=None, scale=None, y
         _arg("lens", lens, dev, torch.int32, (B,)),
         None if pages is None else _arg("pages", pages, dev, torch.int32, (B, Hkv, n_sel)), n_sel, B, Hq, Hkv, d, max_pages,
         num_pages, page_size, d ** -0.5 if scale is None else scale, _dt(q), _dt(y), _arg("y", y, dev, y.dtype, (B, Hq, d)),
-        workspace.data_ptr(), _size(workspace), _now()))
+        workspace.data_ptr(), _size(workspace), _now(dev)))
     return y
 
 
@@ -567,7 +567,7 @@ def attn_page_mean(k_cache, page_table, lens, page_mean=None, starts=None):
         _arg("k_cache", k_cache, dev, k_cache.dtype, (num_pages, Hkv, page_size, d)),
         _arg("page_table", page_table, dev, torch.int32, (B, max_pages)), _arg("lens", lens, dev, torch.int32, (B,)),
         None if starts is None else _arg("starts", starts, dev, torch.int32, (B,)), B, Hkv, d, max_pages, num_pages, page_size,
-        _dt(k_cache), _arg("page_mean", page_mean, dev, torch.float32, (num_pages, Hkv, d)), _now()))
+        _dt(k_cache), _arg("page_mean", page_mean, dev, torch.float32, (num_pages, Hkv, d)), _now(dev)))
     return page_mean
 
 
@@ -585,5 +585,5 @@ def attn_select(q, page_mean, page_table, lens, page_size, n_sel, n_first=0, n_l
         _arg("q", q, dev, q.dtype, (B, Hq, d)), _arg("page_mean", page_mean, dev, torch.float32, (num_pages, Hkv, d)),
         _arg("page_table", page_table, dev, torch.int32, (B, max_pages)), _arg("lens", lens, dev, torch.int32, (B,)), B, Hq,
         Hkv, d, max_pages, num_pages, page_size, n_sel, n_first, n_last, _dt(q),
-        _arg("pages", pages, dev, torch.int32, (B, Hkv, n_sel)), workspace.data_ptr(), _size(workspace), _now()))
+        _arg("pages", pages, dev, torch.int32, (B, Hkv, n_sel)), workspace.data_ptr(), _size(workspace), _now(dev)))
     return pages
