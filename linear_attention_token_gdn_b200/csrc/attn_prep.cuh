@@ -11,9 +11,9 @@
 //
 // Bound by HBM: each row is read once and written once (backward: two rows read, one written).  A row
 // is shared by d/16 lanes, and a lane holds two chunks of 8 channels: the rotating lanes chunk l of
-// both halves of the rotated part, so that both members of a pair are in one lane, the others two
-// adjacent chunks behind it.  Every access is then 16 bytes wide, and the only exchange between lanes
-// is the sum of squares.  A unit (one token, up to `hps` heads of one of the tensors) computes its
+// both halves of the rotated part, so that both members of a pair are in one lane, the others of both
+// halves of the part behind it.  Every access is then 16 bytes wide and next to its neighbours', and the
+// only exchange between lanes is the sum of squares.  A unit (one token, up to `hps` heads of one of the tensors) computes its
 // angles once for its heads, and keeps U rows in flight: a row's registers are loaded again as soon as it
 // is unpacked.  Angles are reduced in fp64, in revolutions: a position of 2^20 leaves an fp32 angle
 // only a few bits behind the point, while position * inv_freq / (2 pi) minus its nearest integer is exact
@@ -43,16 +43,17 @@ struct AttnPrepArgs {
     int num_seqs, max_pages, num_pages, page_size;
 };
 
-// The two chunks of 8 channels that lane `l` of a row holds, and whether they are a rotated pair.
-__device__ __forceinline__ bool attn_chunks(int l, int rot, int& i0, int& j0) {
+// The two chunks of 8 channels that lane `l` of a row of d channels holds: chunk l of both halves of the rotated part,
+// or of both halves of the part behind it.  Whether they are a rotated pair.
+__device__ __forceinline__ bool attn_chunks(int l, int d, int rot, int& i0, int& j0) {
     const int rl = rot >> 4;
     if (l < rl) {
         i0 = 8 * l;
         j0 = i0 + (rot >> 1);
         return true;
     }
-    i0 = 16 * l;
-    j0 = i0 + 8;
+    i0 = rot + 8 * (l - rl);
+    j0 = i0 + ((d - rot) >> 1);
     return false;
 }
 
@@ -69,28 +70,67 @@ __device__ __forceinline__ void attn_turn(int phase, float& c, float& s) {
     c = __uint_as_float(__float_as_uint(c0) ^ ((quarter + 1) << 30 & 0x80000000u));
 }
 
-// The lane's 8 frequencies in revolutions per position (0 where it does not turn).
-__device__ __forceinline__ void attn_revs(const double* inv_freq, int i0, bool turns, double (&f)[8]) {
+// cos and sin of position * inv_freq for the lane's 8 pairs.  Adding and taking away 1.5 * 2^52 rounds to whole
+// revolutions, the fused products leave the rest with one rounding, and adding 1.5 * 2^20 puts it, in units of 2^-32,
+// into the low word: three steps of the fp64 pipe and no conversion instruction, which run at a quarter of its rate and less.
+__device__ __forceinline__ void attn_angles(const double* inv_freq, int i0, bool turns, int position, float2 (&c)[4],
+                                            float2 (&s)[4]) {
+    const double p = (double)position;
+    auto turn = [&](double f, float& cu, float& su) {
+        f *= 0.15915494309189533577;
+        const double whole = __dadd_rn(__fma_rn(p, f, 0x1.8p52), -0x1.8p52);
+        attn_turn(__double2loint(__dadd_rn(__fma_rn(p, f, -whole), 0x1.8p20)), cu, su);
+    };
 #pragma unroll
-    for (int u = 0; u < 8; u += 2) {
-        double2 v = make_double2(0.0, 0.0);
-        if (turns) v = *reinterpret_cast<const double2*>(inv_freq + i0 + u);
-        f[u] = v.x * 0.15915494309189533577;
-        f[u + 1] = v.y * 0.15915494309189533577;
+    for (int u = 0; u < 4; ++u) {
+        c[u] = make_float2(1.0f, 1.0f);
+        s[u] = make_float2(0.0f, 0.0f);
+        if (turns) {
+            const double2 f = *reinterpret_cast<const double2*>(inv_freq + i0 + 2 * u);
+            turn(f.x, c[u].x, s[u].x);
+            turn(f.y, c[u].y, s[u].y);
+        }
     }
 }
 
-// cos and sin of the lane's 8 angles.  Adding and taking away 1.5 * 2^52 rounds to whole revolutions, the fused
-// products leave the rest with one rounding, and adding 1.5 * 2^20 puts it, in units of 2^-32, into the low word: three
-// steps of the fp64 pipe and no conversion instruction, which run at a quarter of its rate and less.
-__device__ __forceinline__ void attn_angles(const double (&f)[8], int position, float (&c)[8], float (&s)[8]) {
-    const double p = (double)position;
+__device__ __forceinline__ void attn_angles(const double* inv_freq, int i0, bool turns, int position, float (&c)[8],
+                                            float (&s)[8]) {
+    float2 c2[4], s2[4];
+    attn_angles(inv_freq, i0, turns, position, c2, s2);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const double whole = __dadd_rn(__fma_rn(p, f[u], 0x1.8p52), -0x1.8p52);
-        attn_turn(__double2loint(__dadd_rn(__fma_rn(p, f[u], -whole), 0x1.8p20)), c[u], s[u]);
+    for (int u = 0; u < 4; ++u) {
+        c[2 * u] = c2[u].x, c[2 * u + 1] = c2[u].y;
+        s[2 * u] = s2[u].x, s[2 * u + 1] = s2[u].y;
     }
 }
+
+// 1 + w for 8 channels.
+__device__ __forceinline__ void attn_weights(const float* w, int i0, float2 (&x)[4]) {
+#pragma unroll
+    for (int u = 0; u < 4; u += 2) {
+        const float4 v = *reinterpret_cast<const float4*>(w + i0 + 2 * u);
+        x[u] = make_float2(1.0f + v.x, 1.0f + v.y);
+        x[u + 1] = make_float2(1.0f + v.z, 1.0f + v.w);
+    }
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{.reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mul.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{.reg .b64 ra, rb, rc, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mov.b64 rc, {%6, %7};\n"
+        " fma.rn.f32x2 rd, ra, rb, rc;\n mov.b64 {%0, %1}, rd;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // A lane's 16 channels of a row as they lie in memory.
 template <int IN>
@@ -106,25 +146,34 @@ struct AttnRow {
             w[Q / 2 + q] = reinterpret_cast<const uint4*>(p + j0)[q];
         }
     }
-    __device__ __forceinline__ void get(float (&xi)[8], float (&xj)[8]) const {
+    __device__ __forceinline__ void get(float2 (&xi)[4], float2 (&xj)[4]) const {
         half(0, xi);
         half(Q / 2, xj);
     }
 
+    __device__ __forceinline__ void get(float (&xi)[8], float (&xj)[8]) const {
+        float2 i[4], j[4];
+        get(i, j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            xi[2 * u] = i[u].x, xi[2 * u + 1] = i[u].y;
+            xj[2 * u] = j[u].x, xj[2 * u + 1] = j[u].y;
+        }
+    }
+
   private:
-    __device__ __forceinline__ void half(int q0, float (&x)[8]) const {
+    __device__ __forceinline__ void half(int q0, float2 (&x)[4]) const {
 #pragma unroll
         for (int q = 0; q < Q / 2; ++q) {
-            const uint32_t v[4] = {w[q0 + q].x, w[q0 + q].y, w[q0 + q].z, w[q0 + q].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (IN == kF32) {
-                    x[4 * q + e] = __uint_as_float(v[e]);
-                } else {
-                    const float2 f = unpack2<IN == kBF16>(v[e]);
-                    x[2 * e] = f.x;
-                    x[2 * e + 1] = f.y;
-                }
+            const uint4 v = w[q0 + q];
+            if constexpr (IN == kF32) {
+                x[2 * q] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+                x[2 * q + 1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+            } else {
+                x[0] = unpack2<IN == kBF16>(v.x);
+                x[1] = unpack2<IN == kBF16>(v.y);
+                x[2] = unpack2<IN == kBF16>(v.z);
+                x[3] = unpack2<IN == kBF16>(v.w);
             }
         }
     }
@@ -143,10 +192,11 @@ __device__ __forceinline__ float attn_row_sum(float x, unsigned mask) {
     return x;
 }
 
-__device__ __forceinline__ void attn_store8(void* p, int dt, size_t i, const float (&x)[8]) {
-    if (dt == kBF16) stv<kBF16, 8>(p, i, x);
-    else if (dt == kF16) stv<kF16, 8>(p, i, x);
-    else stv<kF32, 8>(p, i, x);
+__device__ __forceinline__ void attn_store8(void* p, int dt, size_t i, const float2 (&x)[4]) {
+    const float f[8] = {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y};
+    if (dt == kBF16) stv<kBF16, 8>(p, i, f);
+    else if (dt == kF16) stv<kF16, 8>(p, i, f);
+    else stv<kF32, 8>(p, i, f);
 }
 
 // Physical page of the logical page `page` of row b; -1 (flagged) when the table names none.
@@ -197,7 +247,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
     const size_t x0 = (size_t)t * (size_t)(keys ? a.k_stride : a.q_stride) + (size_t)h0 * D;
     const size_t v0 = CACHE && keys ? (size_t)t * (size_t)a.v_stride + (size_t)h0 * D : 0;
     int i0, j0;
-    const bool turns = attn_chunks(l, a.rot, i0, j0);
+    const bool turns = attn_chunks(l, D, a.rot, i0, j0);
 
     AttnRow<IN> buf[U];
     auto fetch = [&](AttnRow<IN>& to, int m) {
@@ -223,7 +273,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
             dst_step = (size_t)a.page_size * D;
         }
     }
-    auto put = [&](void* out, int m, const float (&yi)[8], const float (&yj)[8]) {
+    auto put = [&](void* out, int m, const float2 (&yi)[4], const float2 (&yj)[4]) {
         const size_t o = dst0 + (size_t)m * dst_step;
         if constexpr (CACHE) {
             const long long cache = (long long)a.num_pages * a.Hkv * a.page_size * D;
@@ -233,46 +283,46 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
         attn_store8(out, a.out_dt, o + j0, yj);
     };
 
-    // y_i = r (x_i ci - x_j sj), y_j = r (x_j cj + x_i si), with 1 + w and the rotation in one factor each
-    float ci[8], cj[8], si[8], sj[8];
+    // y_i = r (x_i ci + x_j mj), y_j = r (x_j cj + x_i si): 1 + w and the rotation in one factor each
+    float2 ci[4], cj[4], si[4], mj[4];
+    attn_angles(a.inv_freq, i0, turns, position, ci, si);
     {
-        double f[8];
-        attn_revs(a.inv_freq, i0, turns, f);
-        attn_angles(f, position, ci, si);
-        const float* w = keys ? a.w_k : a.w_q;
+        float2 wi[4], wj[4];
+        attn_weights(keys ? a.w_k : a.w_q, i0, wi);
+        attn_weights(keys ? a.w_k : a.w_q, j0, wj);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const float wi = 1.0f + w[i0 + u], wj = 1.0f + w[j0 + u];
-            sj[u] = si[u] * wj;
-            cj[u] = ci[u] * wj;
-            si[u] *= wi;
-            ci[u] *= wi;
+        for (int u = 0; u < 4; ++u) {
+            cj[u] = mul2(ci[u], wj[u]);
+            mj[u] = mul2(make_float2(-si[u].x, -si[u].y), wj[u]);
+            ci[u] = mul2(ci[u], wi[u]);
+            si[u] = mul2(si[u], wi[u]);
         }
     }
     for (int hb = 0; hb < rows; hb += U) {
 #pragma unroll
         for (int m = 0; m < U; ++m) {
             if (hb + m >= rows) break;
-            float xi[8], xj[8], ss = 0.0f, st = 0.0f;
+            float2 xi[4], xj[4];
             buf[m].get(xi, xj);
             if (hb + U + m < rows) fetch(buf[m], hb + U + m);
             if (CACHE && hb + m >= n) {  // values go as they are
                 put(a.v_out, hb + m - n, xi, xj);
                 continue;
             }
+            float2 ss = mul2(xi[0], xi[0]), st = mul2(xj[0], xj[0]);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                ss = fmaf(xi[u], xi[u], ss);
-                st = fmaf(xj[u], xj[u], st);
+            for (int u = 1; u < 4; ++u) {
+                ss = fma2(xi[u], xi[u], ss);
+                st = fma2(xj[u], xj[u], st);
             }
-            const float r = rsqrtf(attn_row_sum<LPR>(ss + st, mask) * (1.0f / D) + a.eps);
-            float yi[8], yj[8];
+            const float2 r = both(rsqrtf(attn_row_sum<LPR>((ss.x + st.x) + (ss.y + st.y), mask) * (1.0f / D) + a.eps));
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                yi[u] = r * (xi[u] * ci[u] - xj[u] * sj[u]);
-                yj[u] = r * (xj[u] * cj[u] + xi[u] * si[u]);
+            for (int u = 0; u < 4; ++u) {
+                const float2 yi = mul2(r, fma2(xj[u], mj[u], mul2(xi[u], ci[u])));
+                xj[u] = mul2(r, fma2(xi[u], si[u], mul2(xj[u], cj[u])));
+                xi[u] = yi;
             }
-            put(keys ? a.k_out : a.q_out, hb + m, yi, yj);
+            put(keys ? a.k_out : a.q_out, hb + m, xi, xj);
         }
     }
 }
@@ -312,7 +362,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1
     const float* w = keys ? a.w_k : a.w_q;
 
     int i0, j0;
-    const bool turns = attn_chunks(l, a.rot, i0, j0);
+    const bool turns = attn_chunks(l, D, a.rot, i0, j0);
     float wi[8], wj[8], dwi[8], dwj[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -336,11 +386,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1
             }
         }
         float cs[8], sn[8];
-        {
-            double f[8];
-            attn_revs(a.inv_freq, i0, turns, f);
-            attn_angles(f, a.positions[t], cs, sn);
-        }
+        attn_angles(a.inv_freq, i0, turns, a.positions[t], cs, sn);
         for (int hb = 0; hb < n; hb += U) {
 #pragma unroll
             for (int m = 0; m < U; ++m) {
