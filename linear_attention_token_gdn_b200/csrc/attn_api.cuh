@@ -143,6 +143,12 @@ bool attn_head_dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128 
 
 // ---------------------------------------------------------------- decode
 
+// Whether a pair is left to one CTA, given the most tiles of 16 keys that it can have: up to 256 keys always, up to 512
+// when there are 64 pairs and more.  Measured (us, one CTA a pair against pieces and a join; d = 128): 1 row of 2 key heads,
+// 256 keys 7.7 / 8.5, 512 keys 10.8 / 8.3; 8 rows of 8 key heads, 512 keys 10.8 / 15.9, 1024 keys 21.5 / 18.6; 64 rows of 8,
+// 512 keys 27.8 / 28.6, 1024 keys 47.0 / 40.6.
+bool attn_alone(long long tiles, long long pairs) { return tiles <= (pairs >= 64 ? 32 : 16); }
+
 template <bool BF, int D, int NT, bool CHOSEN>
 gdn_status_t attn_decode_run(gdn::AttnDecodeArgs a, const DeviceInfo& dev, cudaStream_t st) {
     using S = gdn::AttnShape<D, NT>;
@@ -158,11 +164,17 @@ gdn_status_t attn_decode_run(gdn::AttnDecodeArgs a, const DeviceInfo& dev, cudaS
         per_sm.store(n < 1 ? 1 : n, std::memory_order_relaxed);
         ready.fetch_or(bit, std::memory_order_release);
     }
+    const long long pairs = (long long)a.B * a.Hkv * a.hblocks;
+    // Rows that can hold only a few keys are not cut up: a CTA takes a pair, without looking for its place and without a
+    // join behind it.
+    const long long most = a.pages != nullptr ? (long long)a.n_sel * a.tiles_per_page : (long long)a.max_pages * a.tiles_per_page;
+    a.alone = attn_alone(most, pairs) && pairs < (1LL << 31);
+    if (a.alone)
+        return launch_after("attn_decode_kernel", kernel, dim3((unsigned)pairs), dim3(gdn::kAttnThreads), S::SMEM, st, a);
     int ctas = dev.sms * per_sm.load(std::memory_order_relaxed);
     if (ctas > gdn::kAttnMaxCtas) ctas = gdn::kAttnMaxCtas;
     // few pairs: many pieces each, so one head per block and sixteen warps over its pieces, and a block per pair: one
     // per CTA would be mostly blocks without a pair
-    const long long pairs = (long long)a.B * a.Hkv * a.hblocks;
     a.by_pair = pairs * 4 < ctas;
     gdn_status_t r = launch_after("attn_decode_kernel", kernel, dim3((unsigned)ctas), dim3(gdn::kAttnThreads), S::SMEM, st, a);
     if (r != GDN_OK) return r;

@@ -123,6 +123,7 @@ struct AttnDecodeArgs {
     // join).  Otherwise [CTA][2], the pair whose first piece the CTA holds (-1: none, or the only one) and their number.
     int* meta;
     int by_pair;
+    int alone;                                  // one CTA per pair, no piece
     float* part;                                // [grid][2][8 NT][D + 2]: o, then m and l (log2 scale)
 };
 
@@ -188,25 +189,34 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
     for (int b = cta; b < a.B; b += gridDim.x) {
         if (a.lens[b] <= 0) {
             for (int i = tid; i < a.Hq * D; i += kAttnThreads) st1(a.y, a.y_dt, (size_t)b * a.Hq * D + i, 0.0f);
-            if (a.by_pair)
+            if (a.by_pair && !a.alone)
                 for (int i = tid; i < pairs; i += kAttnThreads) a.meta[2 * (b * pairs + i) + 1] = 0;
         }
     }
 
-    long long share = 0;
-    AttnPlace place = attn_locate<kAttnThreads>(
-        a.B, [&](int b) { return (long long)attn_tiles(a, b, attn_len(a.lens, b, capacity)) * pairs; },
-        [&](long long total) {
-            share = (total + gridDim.x - 1) / gridDim.x;
-            share = (share + kAttnMinTiles - 1) / kAttnMinTiles * kAttnMinTiles;
-            return share * cta;
-        });
-    long long at = share * cta;
-    const long long end = at + share < place.total ? at + share : place.total;
+    long long share = 1, at, end, row_base;              // row_base: the line's index of b's first tile
+    int b;
+    if (a.alone) {
+        b = cta / pairs;
+        const int tiles = attn_tiles(a, b, attn_len(a.lens, b, capacity));
+        row_base = 0;
+        at = (long long)(cta - b * pairs) * tiles;
+        end = at + tiles;
+    } else {
+        const AttnPlace place = attn_locate<kAttnThreads>(
+            a.B, [&](int row) { return (long long)attn_tiles(a, row, attn_len(a.lens, row, capacity)) * pairs; },
+            [&](long long total) {
+                share = (total + gridDim.x - 1) / gridDim.x;
+                share = (share + kAttnMinTiles - 1) / kAttnMinTiles * kAttnMinTiles;
+                return share * cta;
+            });
+        at = share * cta;
+        end = at + share < place.total ? at + share : place.total;
+        b = place.b;
+        row_base = place.before;
+    }
     int starting = -1, pieces = 0;
 
-    int b = place.b;
-    long long row_base = place.before;                   // the line's index of b's first tile
     while (at < end) {                                   // one (row, key head, head block) piece per turn
         int len = attn_len(a.lens, b, capacity);
         int tiles = attn_tiles(a, b, len);
@@ -309,6 +319,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
         }
         while (n_keys > 0) {
             const int n_now = n_keys;
+            tile += kAttnWarps;
+            advance();  // the next tile's place is looked up while this one's keys are on their way
             float s[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -321,8 +333,6 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
                     wm::mma16816x<BF>(s[n], hi, qf[n][c][2], qf[n][c][3]);
                 }
             }
-            tile += kAttnWarps;
-            advance();
             if (n_keys > 0) load_k(base, n_keys);
 
             // lane (g, t): keys g (0, 1) and g + 8 (2, 3) of heads 2 t and 2 t + 1
@@ -414,7 +424,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
         }
         __syncthreads();
         const bool whole = first == 0 && last == tiles;
-        if (first == 0) {
+        if (first == 0 && !a.alone) {
             const int last_cta = (int)((row_base + (long long)(pair + 1) * tiles - 1) / share);
             if (!whole) {
                 starting = b * pairs + pair;
@@ -453,21 +463,21 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
         }
         at += last - first;
     }
-    if (!a.by_pair && tid == 0) {
+    if (!a.by_pair && !a.alone && tid == 0) {
         a.meta[2 * cta] = starting;
         a.meta[2 * cta + 1] = pieces;
     }
 }
 
 // Joins the pieces of a (row, key head, head block) that several CTAs share: y = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
-// M = max m_i.  CTA x takes pair x (by_pair), or the pair whose first piece CTA x of the first kernel held, blockIdx.y at `per` heads of
-// it, with W / per warps a head, each taking every (W / per)-th piece.  M and the weights' sum come first, from all pieces
-// at once, so that the loads of the o_i do not wait for one another.
+// M = max m_i.  CTA x takes pair x (by_pair), or the pair whose first piece CTA x of the first kernel held, blockIdx.y
+// `per` heads of it, with W / per warps a head, each taking every (W / per)-th piece, BATCH of them loaded together.
 template <int D, int NT, int W>
 __global__ void __launch_bounds__(32 * W) attn_join_kernel(const AttnDecodeArgs a, int ctas, int per) {
     using S = AttnShape<D, NT>;
     constexpr int E = D / 32, V = E < 4 ? E : 4;  // channels of a lane, of one load
-    __shared__ float s_o[W][D];
+    constexpr int BATCH = E < 8 ? 8 : 6;
+    __shared__ float s_o[W][D], s_m[W], s_l[W];
     tc::wait_prerequisites();
     const int held = a.meta[2 * blockIdx.x], pieces = a.meta[2 * blockIdx.x + 1];
     const int row = a.by_pair ? blockIdx.x : held, cta0 = a.by_pair ? held : blockIdx.x;
@@ -478,57 +488,79 @@ __global__ void __launch_bounds__(32 * W) attn_join_kernel(const AttnDecodeArgs 
     const int heads = min(S::HB, a.group - hb * S::HB);
     const int strides = W / per;
     const int h = blockIdx.y * per + warp % per, sub = warp / per;
-    const bool live = h < heads;
-    auto piece = [&](int i) { return a.part + ((size_t)(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * S::PIECE; };
+    const size_t y0 = ((size_t)b * a.Hq + hk * a.group + hb * S::HB + h) * D;
     float top = -INFINITY, sum = 0.0f, y[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) y[e] = 0.0f;
-    if (live) {
-#pragma unroll 4
-        for (int i = lane; i < pieces; i += 32) {
-            const float2 ml = *reinterpret_cast<const float2*>(piece(i) + S::HB * D + 2 * h);
-            const float next = fmaxf(top, ml.x);
-            if (next != -INFINITY) sum = sum * exp2f(top - next) + (ml.x == -INFINITY ? 0.0f : ml.y * exp2f(ml.x - next));
+    if (h < heads) {
+        for (int i0 = sub; i0 < pieces; i0 += strides * BATCH) {
+            float m[BATCH], lsum[BATCH], o[BATCH][E];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const int i = i0 + u * strides;
+                m[u] = -INFINITY;
+                lsum[u] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[u][e] = 0.0f;
+                if (i < pieces) {
+                    const float* p = a.part + ((size_t)(cta0 + i) * 2 + (i == 0 ? 1 : 0)) * S::PIECE;
+                    const float2 ml = *reinterpret_cast<const float2*>(p + S::HB * D + 2 * h);
+                    m[u] = ml.x;
+                    lsum[u] = ml.y;
+#pragma unroll
+                    for (int e = 0; e < E; e += V) {
+                        if constexpr (V == 4) *reinterpret_cast<float4*>(&o[u][e]) = *reinterpret_cast<const float4*>(p + h * D + 32 * e + 4 * lane);
+                        else if constexpr (V == 2) *reinterpret_cast<float2*>(&o[u][e]) = *reinterpret_cast<const float2*>(p + h * D + 2 * lane);
+                        else o[u][e] = p[h * D + lane];
+                    }
+                }
+            }
+            float next = top;
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) next = fmaxf(next, m[u]);
+            const float f0 = top == -INFINITY ? 0.0f : exp2f(top - next);
+            sum *= f0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] *= f0;
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const float f = m[u] == -INFINITY ? 0.0f : exp2f(m[u] - next);
+                sum = fmaf(f, lsum[u], sum);
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = fmaf(f, o[u][e], y[e]);
+            }
             top = next;
         }
-        const float mine = top;
+    }
+    if (strides == 1) {
+        if (h < heads) {
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // no key left: zeros
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        sum = mine == -INFINITY ? 0.0f : sum * exp2f(mine - top);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll 4
-        for (int i = sub; i < pieces; i += strides) {
-            const float* p = piece(i);
-            const float m = p[S::HB * D + 2 * h], f = m == -INFINITY ? 0.0f : exp2f(m - top);
-#pragma unroll
-            for (int e = 0; e < E; e += V) {
-                float x[V];
-                if constexpr (V == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(p + h * D + 32 * e + 4 * lane);
-                else if constexpr (V == 2) *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p + h * D + 2 * lane);
-                else x[0] = p[h * D + lane];
-#pragma unroll
-                for (int u = 0; u < V; ++u) y[e + u] = fmaf(f, x[u], y[e + u]);
-            }
+            for (int e = 0; e < E; ++e) st1(a.y, a.y_dt, y0 + 32 * (e / V * V) + V * lane + e % V, y[e] * inv);
         }
+        return;
     }
-    if (strides > 1) {
+    // one head (per = 1): its warps' sums side by side, then one thread a channel
 #pragma unroll
-        for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = y[e];
-        __syncthreads();
-        if (sub == 0) {
-            for (int w = per + warp; w < W; w += per) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) y[e] += s_o[w][lane + 32 * e];
-            }
-        }
+    for (int e = 0; e < E; ++e) s_o[warp][32 * (e / V * V) + V * lane + e % V] = y[e];
+    if (lane == 0) {
+        s_m[warp] = top;
+        s_l[warp] = sum;
     }
-    if (sub == 0 && live) {
-        const size_t at = ((size_t)b * a.Hq + hk * a.group + hb * S::HB + h) * D;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // no key left: zeros
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c >= D || h >= heads) return;
+    top = s_m[0];
 #pragma unroll
-        for (int e = 0; e < E; ++e) st1(a.y, a.y_dt, at + 32 * (e / V * V) + V * lane + e % V, y[e] * inv);
+    for (int w = 1; w < W; ++w) top = fmaxf(top, s_m[w]);
+    float total = 0.0f, yc = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const float f = s_m[w] == -INFINITY ? 0.0f : exp2f(s_m[w] - top);
+        total = fmaf(f, s_l[w], total);
+        yc = fmaf(f, s_o[w][c], yc);
     }
+    st1(a.y, a.y_dt, ((size_t)b * a.Hq + hk * a.group + hb * S::HB + blockIdx.y) * D + c, total == 0.0f ? 0.0f : yc / total);
 }
 
 }  // namespace gdn

@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1
     constexpr int LPR = D / 16, SUBS = kAttnPrepThreads / LPR, WARPS = kAttnPrepThreads / 32;
     constexpr int U = IN == kF32 ? 1 : 2;
     __shared__ float s_dw[WARPS][D];
+    __shared__ __align__(16) float s_w[4][LPR][4];
     const int l = threadIdx.x % LPR;
     const unsigned mask = attn_row_mask<LPR>();
     const bool keys = (int)blockIdx.x >= a.gq;
@@ -363,13 +364,25 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1
 
     int i0, j0;
     const bool turns = attn_chunks(l, D, a.rot, i0, j0);
-    float wi[8], wj[8], dwi[8], dwj[8];
+    // 1 + w stays in shared memory (its 16 registers would spill), in the order that the lanes read it
+    float dwi[8], dwj[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        wi[u] = 1.0f + w[i0 + u];
-        wj[u] = 1.0f + w[j0 + u];
-        dwi[u] = dwj[u] = 0.0f;
+    for (int u = 0; u < 8; ++u) dwi[u] = dwj[u] = 0.0f;
+    if (threadIdx.x < LPR) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            s_w[u >> 2][l][u & 3] = 1.0f + w[i0 + u];
+            s_w[2 + (u >> 2)][l][u & 3] = 1.0f + w[j0 + u];
+        }
     }
+    __syncthreads();
+    auto weight = [&](int q, float (&x)[8]) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const float4 f = *reinterpret_cast<const float4*>(s_w[2 * q + v][l]);
+            x[4 * v] = f.x, x[4 * v + 1] = f.y, x[4 * v + 2] = f.z, x[4 * v + 3] = f.w;
+        }
+    };
 
     const unsigned units = (unsigned)a.N * (unsigned)(keys ? a.ck : a.cq);  // < 2^30 (host check)
     for (unsigned unit = (unsigned)blk * SUBS + threadIdx.x / LPR; unit < units; unit += (unsigned)blocks * SUBS) {
@@ -399,7 +412,9 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1
                     gb[m].load(dy, g0 + (size_t)(hb + U + m) * D, i0, j0);
                 }
                 // gi, gj become dn, and dot the sum of dn (1 + w) x
-                float ss = 0.0f, dot = 0.0f;
+                float ss = 0.0f, dot = 0.0f, wi[8], wj[8];
+                weight(0, wi);
+                weight(1, wj);
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const float ni = gi[u] * cs[u] + gj[u] * sn[u], nj = gj[u] * cs[u] - gi[u] * sn[u];
@@ -415,6 +430,8 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1
                 }
                 const float r = rsqrtf(ss * (1.0f / D) + a.eps);
                 const float back = r * (r * (dot * r * (1.0f / D)));  // r^2 mean(gn u), of x
+                weight(0, wi);
+                weight(1, wj);
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     gi[u] *= r;

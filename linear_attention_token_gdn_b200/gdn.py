@@ -412,6 +412,8 @@ def _on_stream(fn):
             raise ValueError("libgdn takes device tensors only")
         if stream is None and first.get_device() == torch.cuda.current_device():
             return fn(first, *args, **kwargs)
+        if stream is not None and stream.device != first.device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {first.device}")
         with torch.cuda.device(first.device), torch.cuda.stream(stream):
             return fn(first, *args, **kwargs)
     return call
@@ -424,10 +426,10 @@ def _now(device):
 
 def _arg(name, t, device, dtype, shape):
     """Address of a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} is not a contiguous {dtype} tensor of shape {list(shape)} on {device}: "
-                         f"{t.dtype} {list(t.shape)}, strides {list(t.stride())}, on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} is not a contiguous {dtype} tensor of shape {list(shape)} on {device}: "
+                     f"{t.dtype} {list(t.shape)}, strides {list(t.stride())}, on {t.device}")
 
 
 def _rows(name, t, like, heads=None):
