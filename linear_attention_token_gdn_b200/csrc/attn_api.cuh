@@ -78,10 +78,10 @@ gdn_status_t launch_after(const char* name, void (*kernel)(P...), dim3 grid, dim
 
 // ---------------------------------------------------------------- norm and rotation
 
-// Heads per unit: the most (up to 8) that still give every SM about two blocks.
-int attn_heads_per_unit(long long rows, int lanes, int heads, int sms) {
+// Heads per unit: the most (up to `most`) that still give two CTAs an SM a unit for every group of lanes.
+int attn_heads_per_unit(long long rows, int lanes, int heads, int sms, int most) {
     int hps = 1;
-    while (hps < 8 && hps < heads && rows * lanes / (2 * hps) >= 2LL * sms * gdn::kAttnPrepThreads) hps *= 2;
+    while (hps < most && hps < heads && rows * lanes / (2 * hps) >= 2LL * sms * gdn::kAttnPrepThreads) hps *= 2;
     return hps;
 }
 
@@ -105,9 +105,9 @@ gdn_status_t attn_prep_launch(gdn::AttnPrepArgs& a, int d, int in_dt, cudaStream
     gdn_status_t r = device_info(&dev);
     if (r != GDN_OK) return r;
     const int lanes = d / 16;
-    a.hps = attn_heads_per_unit((long long)a.N * (a.Hq + (CACHE ? 2 : 1) * a.Hkv), lanes, a.Hq, dev.sms);
-    a.cq = (a.Hq + a.hps - 1) / a.hps;
-    a.ck = (a.Hkv + a.hps - 1) / a.hps;
+    const int hps = attn_heads_per_unit((long long)a.N * (a.Hq + (CACHE ? 2 : 1) * a.Hkv), lanes, a.Hq, dev.sms, 16);
+    a.cq = (a.Hq + hps - 1) / hps;
+    a.ck = (a.Hkv + hps - 1) / hps;
     const long long threads = (long long)a.N * (a.cq + a.ck) * lanes;
     const long long grid = (threads + gdn::kAttnPrepThreads - 1) / gdn::kAttnPrepThreads;
     REQUIRE(grid * (gdn::kAttnPrepThreads / lanes) < (1LL << 31) && threads < (1LL << 32) - 256, "N=%d with Hq=%d too large",
@@ -366,7 +366,7 @@ gdn_status_t gdn_attn_prep_bwd(const void* dq_out, const void* dk_out, const voi
     a.w_q = w_q; a.w_k = w_k; a.eps = eps; a.positions = positions; a.inv_freq = inv_freq; a.rot = rot_dim;
     a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.dq = dq; a.dk = dk;
     a.partial = reinterpret_cast<float*>(workspace);
-    a.hps = attn_heads_per_unit((long long)N * (Hq + Hkv), lanes, Hq, dev.sms);
+    a.hps = attn_heads_per_unit((long long)N * (Hq + Hkv), lanes, Hq, dev.sms, 8);
     a.cq = (Hq + a.hps - 1) / a.hps;
     a.ck = (Hkv + a.hps - 1) / a.hps;
     const long long uq = (long long)N * a.cq, uk = (long long)N * a.ck;

@@ -13,7 +13,7 @@
 // is shared by d/16 lanes, and a lane holds two chunks of 8 channels: the rotating lanes chunk l of
 // both halves of the rotated part, so that both members of a pair are in one lane, the others of both
 // halves of the part behind it.  Every access is then 16 bytes wide and next to its neighbours', and the
-// only exchange between lanes is the sum of squares.  A unit (one token, up to `hps` heads of one of the tensors) computes its
+// only exchange between lanes is the sum of squares.  A unit (one token, some heads of one of the tensors) computes its
 // angles once for its heads, and keeps U rows in flight: a row's registers are loaded again as soon as it
 // is unpacked.  Angles are reduced in fp64, in revolutions: a position of 2^20 leaves an fp32 angle
 // only a few bits behind the point, while position * inv_freq / (2 pi) minus its nearest integer is exact
@@ -36,7 +36,7 @@ struct AttnPrepArgs {
     float eps;
     const int32_t* positions;
     const double* inv_freq;
-    int rot, N, Hq, Hkv, hps, cq, ck;           // heads per unit; units per token of q, and of k (with v)
+    int rot, N, Hq, Hkv, cq, ck;                // units per token of q, and of k (with v)
     int out_dt;
     void *q_out, *k_out, *v_out;                // k_out, v_out: the cache when CACHE
     const int32_t *cu, *table;
@@ -233,15 +233,15 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
     constexpr int U = IN == kF32 ? 2 : 4;       // rows in flight
     const int l = threadIdx.x % LPR;
     const unsigned mask = attn_row_mask<LPR>();
-    // all tokens of the first heads, then of the next: a warp's rows then have one tensor and one number of heads
-    const unsigned unit = (blockIdx.x * (unsigned)kAttnPrepThreads + threadIdx.x) / LPR;
-    const int c = (int)(unit / (unsigned)a.N);
-    const int t = (int)(unit - (unsigned)c * (unsigned)a.N);
-    if (c >= a.cq + a.ck) return;
-    const bool keys = c >= a.cq;
-    const int heads = keys ? a.Hkv : a.Hq;
-    const int h0 = (keys ? c - a.cq : c) * a.hps;
-    const int n = min(a.hps, heads - h0);
+    // The queries' units, then the keys'.  A token's units stand side by side and take every `step`-th head, so that
+    // what is under way at a time is contiguous.
+    unsigned unit = (blockIdx.x * (unsigned)kAttnPrepThreads + threadIdx.x) / LPR;
+    const bool keys = unit >= (unsigned)a.N * (unsigned)a.cq;
+    if (keys) unit -= (unsigned)a.N * (unsigned)a.cq;
+    const int heads = keys ? a.Hkv : a.Hq, step = keys ? a.ck : a.cq;
+    const int t = (int)(unit / (unsigned)step), h0 = (int)(unit - (unsigned)t * (unsigned)step);
+    if (t >= a.N) return;
+    const int n = (heads - h0 + step - 1) / step;
     const int rows = CACHE && keys ? 2 * n : n;  // keys, then the same heads' values
     const void* x = keys ? a.k : a.q;
     const size_t x0 = (size_t)t * (size_t)(keys ? a.k_stride : a.q_stride) + (size_t)h0 * D;
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
 
     AttnRow<IN> buf[U];
     auto fetch = [&](AttnRow<IN>& to, int m) {
-        if (CACHE && m >= n) to.load(a.v, v0 + (size_t)(m - n) * D, i0, j0);
-        else to.load(x, x0 + (size_t)m * D, i0, j0);
+        if (CACHE && m >= n) to.load(a.v, v0 + (size_t)((m - n) * step) * D, i0, j0);
+        else to.load(x, x0 + (size_t)(m * step) * D, i0, j0);
     };
 #pragma unroll
     for (int m = 0; m < U; ++m) {
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
     }
     const int position = a.positions[t];
 
-    size_t dst0 = ((size_t)t * heads + h0) * D, dst_step = D;  // of the first head, and from head to head
+    size_t dst0 = ((size_t)t * heads + h0) * D, dst_step = (size_t)step * D;  // of the first head, and to the next
     if constexpr (CACHE) {
         if (position < 0) return;  // a padding token
         const int seq = attn_seq_of(a.cu, a.num_seqs, a.N, t);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
             const int phys = attn_page(a.table, a.max_pages, a.num_pages, seq, page);
             if (phys < 0) return;
             dst0 = (((size_t)phys * a.Hkv + h0) * a.page_size + (position - page * a.page_size)) * D;
-            dst_step = (size_t)a.page_size * D;
+            dst_step = (size_t)(step * a.page_size) * D;
         }
     }
     auto put = [&](void* out, int m, const float2 (&yi)[4], const float2 (&yj)[4]) {
@@ -336,7 +336,7 @@ struct AttnPrepBwdArgs {
     float eps;
     const int32_t* positions;
     const double* inv_freq;
-    int rot, N, Hq, Hkv, hps, cq, ck;
+    int rot, N, Hq, Hkv, hps, cq, ck;           // heads per unit; units per token of q, and of k
     int gq;                                     // blocks of the queries; the others take the keys
     void *dq, *dk;
     float* partial;                             // [blocks, d]: each block's share of dw

@@ -410,7 +410,7 @@ def _on_stream(fn):
     def call(first, *args, stream=None, **kwargs):
         if not first.is_cuda:
             raise ValueError("libgdn takes device tensors only")
-        if stream is None and first.get_device() == torch.cuda.current_device():
+        if stream is None and first.get_device() == torch._C._cuda_getDevice():
             return fn(first, *args, **kwargs)
         if stream is not None and stream.device != first.device:
             raise ValueError(f"a stream of {stream.device} for tensors on {first.device}")
@@ -432,12 +432,12 @@ def _arg(name, t, device, dtype, shape):
                      f"{t.dtype} {list(t.shape)}, strides {list(t.stride())}, on {t.device}")
 
 
-def _rows(name, t, like, heads=None):
+def _rows(name, t, device, dtype, shape):
     """(address, token stride) of [N, H, d] rows: a token's heads contiguous, tokens any stride apart."""
-    N, H, d = t.shape
-    if t.dtype != like.dtype or t.device != like.device or N != like.shape[0] or d != like.shape[2] \
-            or (heads is not None and H != heads):
-        raise ValueError(f"{name} does not go with the other rows: {t.dtype} {list(t.shape)} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} does not go with the other rows: {t.dtype} {list(t.shape)} on {t.device}, not {dtype} "
+                         f"{list(shape)} on {device}")
+    N, H, d = shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d != 1) or (s1 != d and H != 1):
         raise ValueError(f"{name}: a token's heads must be contiguous (strides {s0}, {s1}, {s2})")
@@ -446,22 +446,24 @@ def _rows(name, t, like, heads=None):
 
 def _angles(inv_freq, device):
     """(address, rot_dim) of the rotation's frequencies."""
-    if inv_freq is None or inv_freq.numel() == 0:
-        return None, 0
-    return _arg("inv_freq", inv_freq, device, torch.float64, (inv_freq.numel(),)), 2 * inv_freq.numel()
+    n = 0 if inv_freq is None else inv_freq.numel()
+    return (_arg("inv_freq", inv_freq, device, torch.float64, (n,)), 2 * n) if n else (None, 0)
 
 
 def _room(workspace, nbytes, device):
-    """The caller's workspace, or a new one."""
+    """(workspace, address, bytes): the caller's, or a new one."""
     if workspace is None:
-        return torch.empty(nbytes, device=device, dtype=torch.uint8)
+        workspace = torch.empty(nbytes, device=device, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), nbytes
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("the workspace is not a contiguous tensor on the call's device")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _size(t):
-    return t.numel() * t.element_size()
+@functools.lru_cache(maxsize=256)
+def _room_size(which, *sizes):
+    """gdn_attn_<which>_workspace_size."""
+    return getattr(lib(), f"gdn_attn_{which}_workspace_size")(*sizes)
 
 
 @_on_stream
@@ -470,8 +472,8 @@ def attn_prep(q, k, w_q, w_k, positions, inv_freq, eps=1e-6, out_dtype=None, out
     slices of one projection's output; inv_freq [rot_dim / 2] fp64 (None: no rotation).  Returns (q_out, k_out)."""
     N, Hq, d = q.shape
     Hkv, dev = k.shape[1], q.device
-    qp, qs = _rows("q", q, q)
-    kp, ks = _rows("k", k, q)
+    qp, qs = _rows("q", q, dev, q.dtype, (N, Hq, d))
+    kp, ks = _rows("k", k, dev, q.dtype, (N, Hkv, d))
     fp, rot = _angles(inv_freq, dev)
     if out is None:
         out_dtype = q.dtype if out_dtype is None else out_dtype
@@ -495,9 +497,9 @@ def attn_prep_cache(q, k, v, w_q, w_k, positions, inv_freq, k_cache, v_cache, pa
     Hkv, dev = k.shape[1], q.device
     num_pages, _, page_size, _ = k_cache.shape
     num_seqs, max_pages = page_table.shape
-    qp, qs = _rows("q", q, q)
-    kp, ks = _rows("k", k, q)
-    vp, vs = _rows("v", v, q, Hkv)
+    qp, qs = _rows("q", q, dev, q.dtype, (N, Hq, d))
+    kp, ks = _rows("k", k, dev, q.dtype, (N, Hkv, d))
+    vp, vs = _rows("v", v, dev, q.dtype, (N, Hkv, d))
     fp, rot = _angles(inv_freq, dev)
     dtype = k_cache.dtype
     if q_out is None:
@@ -519,20 +521,20 @@ def attn_prep_bwd(dq_out, dk_out, q, k, w_q, w_k, positions, inv_freq, eps=1e-6,
     in q's dtype, dw_q, dw_k [d] fp32."""
     N, Hq, d = q.shape
     Hkv, dev = k.shape[1], q.device
-    qp, qs = _rows("q", q, q)
-    kp, ks = _rows("k", k, q)
+    qp, qs = _rows("q", q, dev, q.dtype, (N, Hq, d))
+    kp, ks = _rows("k", k, dev, q.dtype, (N, Hkv, d))
     fp, rot = _angles(inv_freq, dev)
     if out is None:
         out = dict(dq=torch.empty(N, Hq, d, device=dev, dtype=q.dtype), dk=torch.empty(N, Hkv, d, device=dev, dtype=q.dtype),
                    dw_q=torch.empty(d, device=dev), dw_k=torch.empty(d, device=dev))
-    workspace = _room(workspace, lib().gdn_attn_prep_bwd_workspace_size(d), dev)
+    workspace, room, nbytes = _room(workspace, _room_size("prep_bwd", d), dev)
     _check(lib().gdn_attn_prep_bwd(
         _arg("dq_out", dq_out, dev, dq_out.dtype, (N, Hq, d)), _arg("dk_out", dk_out, dev, dq_out.dtype, (N, Hkv, d)), qp, kp,
         qs, ks, _arg("w_q", w_q, dev, torch.float32, (d,)), _arg("w_k", w_k, dev, torch.float32, (d,)), eps,
         _arg("positions", positions, dev, torch.int32, (N,)), fp, rot, N, Hq, Hkv, d, _dt(q), _dt(dq_out),
         _arg("dq", out["dq"], dev, q.dtype, (N, Hq, d)), _arg("dk", out["dk"], dev, q.dtype, (N, Hkv, d)),
         _arg("dw_q", out["dw_q"], dev, torch.float32, (d,)), _arg("dw_k", out["dw_k"], dev, torch.float32, (d,)),
-        workspace.data_ptr(), _size(workspace), _now(dev)))
+        room, nbytes, _now(dev)))
     return out
 
 
@@ -543,17 +545,18 @@ def attn_decode(q, k_cache, v_cache, page_table, lens, pages=None, scale=None, y
     B, Hq, d = q.shape
     num_pages, Hkv, page_size, _ = k_cache.shape
     max_pages, dev = page_table.shape[1], q.device
+    qp = _arg("q", q, dev, q.dtype, (B, Hq, d))
     if y is None:
-        y = torch.empty(B, Hq, d, device=dev, dtype=q.dtype if y_dtype is None else y_dtype)
-    workspace = _room(workspace, lib().gdn_attn_decode_workspace_size(Hq, Hkv, d), dev)
+        y = torch.empty_like(q, dtype=y_dtype)
+    workspace, room, nbytes = _room(workspace, _room_size("decode", Hq, Hkv, d), dev)
     cache, n_sel = (num_pages, Hkv, page_size, d), 0 if pages is None else pages.shape[2]
     _check(lib().gdn_attn_decode(
-        _arg("q", q, dev, q.dtype, (B, Hq, d)), _arg("k_cache", k_cache, dev, q.dtype, cache),
+        qp, _arg("k_cache", k_cache, dev, q.dtype, cache),
         _arg("v_cache", v_cache, dev, q.dtype, cache), _arg("page_table", page_table, dev, torch.int32, (B, max_pages)),
         _arg("lens", lens, dev, torch.int32, (B,)),
         None if pages is None else _arg("pages", pages, dev, torch.int32, (B, Hkv, n_sel)), n_sel, B, Hq, Hkv, d, max_pages,
         num_pages, page_size, d ** -0.5 if scale is None else scale, _dt(q), _dt(y), _arg("y", y, dev, y.dtype, (B, Hq, d)),
-        workspace.data_ptr(), _size(workspace), _now(dev)))
+        room, nbytes, _now(dev)))
     return y
 
 
@@ -582,10 +585,10 @@ def attn_select(q, page_mean, page_table, lens, page_size, n_sel, n_first=0, n_l
     max_pages, dev = page_table.shape[1], q.device
     if pages is None:
         pages = torch.empty(B, Hkv, n_sel, device=dev, dtype=torch.int32)
-    workspace = _room(workspace, lib().gdn_attn_select_workspace_size(B, Hkv, max_pages), dev)
+    workspace, room, nbytes = _room(workspace, lib().gdn_attn_select_workspace_size(B, Hkv, max_pages), dev)
     _check(lib().gdn_attn_select(
         _arg("q", q, dev, q.dtype, (B, Hq, d)), _arg("page_mean", page_mean, dev, torch.float32, (num_pages, Hkv, d)),
         _arg("page_table", page_table, dev, torch.int32, (B, max_pages)), _arg("lens", lens, dev, torch.int32, (B,)), B, Hq,
         Hkv, d, max_pages, num_pages, page_size, n_sel, n_first, n_last, _dt(q),
-        _arg("pages", pages, dev, torch.int32, (B, Hkv, n_sel)), workspace.data_ptr(), _size(workspace), _now(dev)))
+        _arg("pages", pages, dev, torch.int32, (B, Hkv, n_sel)), room, nbytes, _now(dev)))
     return pages
