@@ -54,6 +54,19 @@ __device__ __forceinline__ long long warp_scan(long long x) {
 // it and get the same answer.  b = B when the target is not below the total.
 template <int THREADS, class Count, class Target>
 __device__ __forceinline__ AttnPlace attn_locate(int B, Count count, Target target) {
+    if (B <= 32) {  // each warp for itself
+        const int lane = threadIdx.x & 31;
+        const long long n = lane < B ? count(lane) : 0, incl = warp_scan(n);
+        AttnPlace p;
+        p.total = __shfl_sync(0xffffffffu, incl, 31);
+        const long long want = target(p.total);
+        const unsigned hit = __ballot_sync(0xffffffffu, want < incl && want >= incl - n);
+        const int src = hit != 0 ? __ffs(hit) - 1 : 0;
+        const long long before = __shfl_sync(0xffffffffu, incl - n, src);
+        p.b = hit != 0 ? src : B;
+        p.before = hit != 0 ? before : p.total;
+        return p;
+    }
     __shared__ long long s_warp[THREADS / 32];
     __shared__ long long s_before;
     __shared__ int s_b;
@@ -127,9 +140,11 @@ struct AttnDecodeArgs {
     float* part;                                // [grid][2][8 NT][D + 2]: o, then m and l (log2 scale)
 };
 
-// The tiles of row b for one of its (key head, head block) pairs.
-__device__ __forceinline__ int attn_tiles(const AttnDecodeArgs& a, int b, int len) {
-    return a.pages == nullptr ? (len + 15) >> 4 : len > 0 ? a.n_sel * a.tiles_per_page : 0;
+// The tiles of a row of `len` keys for one of its (key head, head block) pairs.  With listed pages every row has the
+// same number, whatever its length.
+template <bool CHOSEN>
+__device__ __forceinline__ int attn_tiles(const AttnDecodeArgs& a, int len) {
+    return CHOSEN ? a.n_sel * a.tiles_per_page : (len + 15) >> 4;
 }
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
@@ -185,8 +200,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
     tc::wait_prerequisites();
     tc::launch_dependents();  // every CTA is resident: the join's take no place from them
 
-    // rows without a key
-    for (int b = cta; b < a.B; b += gridDim.x) {
+    // rows without a key (with listed pages, their tiles are empty instead)
+    for (int b = CHOSEN ? a.B : cta; b < a.B; b += gridDim.x) {
         if (a.lens[b] <= 0) {
             for (int i = tid; i < a.Hq * D; i += kAttnThreads) st1(a.y, a.y_dt, (size_t)b * a.Hq * D + i, 0.0f);
             if (a.by_pair && !a.alone)
@@ -198,33 +213,43 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
     int b;
     if (a.alone) {
         b = cta / pairs;
-        const int tiles = attn_tiles(a, b, attn_len(a.lens, b, capacity));
+        const int tiles = attn_tiles<CHOSEN>(a, CHOSEN ? 0 : attn_len(a.lens, b, capacity));
         row_base = 0;
         at = (long long)(cta - b * pairs) * tiles;
         end = at + tiles;
     } else {
-        const AttnPlace place = attn_locate<kAttnThreads>(
-            a.B, [&](int row) { return (long long)attn_tiles(a, row, attn_len(a.lens, row, capacity)) * pairs; },
-            [&](long long total) {
-                share = (total + gridDim.x - 1) / gridDim.x;
-                share = (share + kAttnMinTiles - 1) / kAttnMinTiles * kAttnMinTiles;
-                return share * cta;
-            });
-        at = share * cta;
-        end = at + share < place.total ? at + share : place.total;
-        b = place.b;
-        row_base = place.before;
+        auto cut = [&](long long total) {
+            share = (total + gridDim.x - 1) / gridDim.x;
+            share = (share + kAttnMinTiles - 1) / kAttnMinTiles * kAttnMinTiles;
+            return share * cta;
+        };
+        long long total;
+        if constexpr (CHOSEN) {
+            const long long row = (long long)attn_tiles<CHOSEN>(a, 0) * pairs;
+            total = row * a.B;
+            at = cut(total);
+            b = at < total ? (int)(at / row) : a.B;
+            row_base = b * row;
+        } else {
+            const AttnPlace place = attn_locate<kAttnThreads>(
+                a.B, [&](int row) { return (long long)attn_tiles<CHOSEN>(a, attn_len(a.lens, row, capacity)) * pairs; }, cut);
+            total = place.total;
+            at = share * cta;
+            b = place.b;
+            row_base = place.before;
+        }
+        end = at + share < total ? at + share : total;
     }
     int starting = -1, pieces = 0;
 
     while (at < end) {                                   // one (row, key head, head block) piece per turn
         int len = attn_len(a.lens, b, capacity);
-        int tiles = attn_tiles(a, b, len);
+        int tiles = attn_tiles<CHOSEN>(a, len);
         while (at >= row_base + (long long)tiles * pairs) {
             row_base += (long long)tiles * pairs;
             ++b;
             len = attn_len(a.lens, b, capacity);
-            tiles = attn_tiles(a, b, len);
+            tiles = attn_tiles<CHOSEN>(a, len);
         }
         const int pair = (int)((at - row_base) / tiles);
         const int hk = pair / a.hblocks, hb = pair - hk * a.hblocks;

@@ -298,7 +298,7 @@ constexpr int kSelectThreads = 256;
 // found by 8-bit digits, from the highest bit in which the keys differ, each digit's counts in shared memory; then come
 // the pages above it and the first ones equal to it, in page order.  The first 2048 pages' keys stay in registers.
 // Latency-bound: one CTA per list, three or four digits of two barriers each.
-__global__ void __launch_bounds__(kSelectThreads) attn_select_kernel(const AttnSelectArgs a) {
+__global__ void __launch_bounds__(kSelectThreads, 4) attn_select_kernel(const AttnSelectArgs a) {
     constexpr int WARPS = kSelectThreads / 32, C = 8, SPAN = C * kSelectThreads;
     static_assert(kSelectThreads == 256, "one thread per digit");
     __shared__ __align__(16) int s_count[2][256];
