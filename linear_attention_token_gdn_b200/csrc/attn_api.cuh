@@ -171,27 +171,32 @@ gdn_status_t attn_decode_run(gdn::AttnDecodeArgs a, const DeviceInfo& dev, cudaS
     a.alone = attn_alone(most, pairs) && pairs < (1LL << 31);
     if (a.alone)
         return launch_after("attn_decode_kernel", kernel, dim3((unsigned)pairs), dim3(gdn::kAttnThreads), S::SMEM, st, a);
-    int ctas = dev.sms * per_sm.load(std::memory_order_relaxed);
-    if (ctas > gdn::kAttnMaxCtas) ctas = gdn::kAttnMaxCtas;
-    // few pairs: many pieces each, so one head per block and sixteen warps over its pieces, and a block per pair: one
-    // per CTA would be mostly blocks without a pair
+    // one resident wave, as far as the workspace reaches (half as far for 16 heads of 256 channels)
+    constexpr int reach = D == 256 && NT == 2 ? gdn::kAttnMaxCtas / 2 : gdn::kAttnMaxCtas;
+    int fit = per_sm.load(std::memory_order_relaxed);
+    if (fit * dev.sms > reach && fit > 1) fit = reach / dev.sms > 1 ? reach / dev.sms : 1;
+    const int ctas = fit * dev.sms < reach ? fit * dev.sms : reach;
+    // few pairs: many pieces each, so one head per block and sixteen warps over its pieces, and blocks by pair: one per
+    // CTA would be mostly blocks without a pair.  Very few: 64 channels of a head per block.
+    constexpr int kSlice = D < 64 ? D : 64;
     a.by_pair = pairs * 4 < ctas;
     gdn_status_t r = launch_after("attn_decode_kernel", kernel, dim3((unsigned)ctas), dim3(gdn::kAttnThreads), S::SMEM, st, a);
     if (r != GDN_OK) return r;
+    if (a.by_pair && pairs * S::HB * (D / kSlice) <= dev.sms)
+        return launch_after("attn_join_kernel", gdn::attn_join_kernel<D, NT, 16, kSlice>, dim3((unsigned)pairs, S::HB, D / kSlice),
+                            dim3(512), 0, st, a, ctas, 1);
     if (a.by_pair)
-        return launch_after("attn_join_kernel", gdn::attn_join_kernel<D, NT, 16>, dim3((unsigned)pairs, (unsigned)S::HB), dim3(512),
-                            0, st, a, ctas, 1);
-    return launch_after("attn_join_kernel", gdn::attn_join_kernel<D, NT, 8>, dim3((unsigned)ctas, (unsigned)NT), dim3(256), 0, st, a,
+        return launch_after("attn_join_kernel", gdn::attn_join_kernel<D, NT, 16, D>, dim3((unsigned)pairs, S::HB), dim3(512), 0, st,
+                            a, ctas, 1);
+    return launch_after("attn_join_kernel", gdn::attn_join_kernel<D, NT, 8, D>, dim3((unsigned)ctas, (unsigned)NT), dim3(256), 0, st, a,
                         ctas, 8);
 }
 
 template <bool BF, int D>
 gdn_status_t attn_decode_d(const gdn::AttnDecodeArgs& a, int nt, const DeviceInfo& dev, cudaStream_t st) {
-    if constexpr (D < 256) {
-        if (nt == 2)
-            return a.pages == nullptr ? attn_decode_run<BF, D, 2, false>(a, dev, st)
-                                      : attn_decode_run<BF, D, 2, true>(a, dev, st);
-    }
+    if (nt == 2)
+        return a.pages == nullptr ? attn_decode_run<BF, D, 2, false>(a, dev, st)
+                                  : attn_decode_run<BF, D, 2, true>(a, dev, st);
     return a.pages == nullptr ? attn_decode_run<BF, D, 1, false>(a, dev, st) : attn_decode_run<BF, D, 1, true>(a, dev, st);
 }
 
@@ -207,9 +212,8 @@ gdn_status_t attn_decode_bf(const gdn::AttnDecodeArgs& a, int d, int nt, const D
 
 bool attn_decode_dim_ok(int d) { return d == 32 || d == 64 || d == 128 || d == 256; }
 
-// Query-head tiles of 8 that a CTA takes together: two for groups above 8 (the keys are then read once for 16), but
-// one at d = 256, where two tiles' accumulators would spill (680 bytes a thread).
-int attn_head_tiles(int group, int d) { return group > 8 && d < 256 ? 2 : 1; }
+// Query-head tiles of 8 that a CTA takes together: two for groups above 8, as the keys are then read once for 16.
+int attn_head_tiles(int group) { return group > 8 ? 2 : 1; }
 
 constexpr size_t kAttnMetaBytes = (size_t)gdn::kAttnMaxCtas * 2 * sizeof(int);
 
@@ -395,8 +399,9 @@ gdn_status_t gdn_attn_prep_bwd(const void* dq_out, const void* dk_out, const voi
 
 size_t gdn_attn_decode_workspace_size(int Hq, int Hkv, int d) {
     if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !attn_decode_dim_ok(d)) return 0;
-    const int nt = attn_head_tiles(Hq / Hkv, d);
-    return kAttnMetaBytes + (size_t)gdn::kAttnMaxCtas * 2 * 8 * nt * (d + 2) * sizeof(float);
+    const int nt = attn_head_tiles(Hq / Hkv);
+    const size_t ctas = d == 256 && nt == 2 ? gdn::kAttnMaxCtas / 2 : gdn::kAttnMaxCtas;  // as many as are launched
+    return kAttnMetaBytes + ctas * 2 * 8 * nt * (d + 2) * sizeof(float);
 }
 
 gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
@@ -425,7 +430,7 @@ gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_c
     gdn_status_t r = device_info(&dev);
     if (r != GDN_OK) return r;
     gdn::AttnDecodeArgs a{};
-    const int nt = attn_head_tiles(Hq / Hkv, d);
+    const int nt = attn_head_tiles(Hq / Hkv);
     a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.table = page_table; a.lens = lens; a.pages = pages;
     a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.group = Hq / Hkv; a.hblocks = (a.group + 8 * nt - 1) / (8 * nt);
     a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages; a.n_sel = pages != nullptr ? n_sel : 0;

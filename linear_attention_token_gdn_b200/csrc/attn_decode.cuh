@@ -14,12 +14,11 @@
 // small kernel joins them in the order of the line, so results do not depend on timing.
 //
 // Tile.  A warp takes 16 keys at a time, S^T = K Q^T and O^T = V^T P^T by mma.sync m16n8k16: the group's
-// query heads are the 8 columns (16 in two tiles), so a group of 8 wastes nothing, and no operand goes
-// through shared memory.  The contraction runs over channels in any order, so a lane's part of K, 4
-// channels out of 16, is 8 adjacent channels for two steps: a 16-byte load gives both.  The same for V
-// with two keys' words interleaved by byte permutes (the fragment wants adjacent keys of one channel).
-// P goes from the accumulators to the B operand by movmatrix.  The K registers are refilled as soon as
-// S is formed, the V registers as soon as O is updated, so a warp always has 4 to 8 KB (d = 128) in flight.
+// query heads are the 8 columns (16 in two tiles), so a group of 8 wastes nothing.  Each warp has a ring of its own in
+// shared memory, of 3 slots of 16 keys or values, which its lanes fill by 16-byte asynchronous copies, so that two slots
+// (8 KB at d = 128) a warp are under way whatever the registers hold, and nothing waits for another warp.  Chunks of a row are swizzled by the row, and ldmatrix (transposed for V) delivers the fragments without
+// bank conflicts.  Q lies there too: it would take up to 64 registers.  P goes from the accumulators to the B operand by
+// movmatrix.  Places behind the row's last key are filled with zeros instead of being read.
 // P enters as a 16-bit value and its 16-bit remainder: a single rounding (2^-9 for bf16) would add as much
 // error as the output's own rounding, and the tensor pipe has the room.
 // m follows the scores lazily: it moves only when a score exceeds it by more than 8 (in log2), so p is at
@@ -161,36 +160,40 @@ __device__ __forceinline__ void split16(float x0, float x1, uint32_t& hi, uint32
     lo = pack2<BF>(x0 - f.x, x1 - f.y);
 }
 
-// 4 or 2 words of a cache row, read once: no line of it is kept in L1.
-template <int W>
-__device__ __forceinline__ void ld_stream(const void* p, uint32_t* r) {
-    if constexpr (W == 4)
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                     : "l"(p));
-    else
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
-}
-
 template <int D, int NT>
 struct AttnShape {
-    static constexpr int KC = D / 32;                    // 16-byte loads of a key per lane
-    static constexpr int VW = D >= 64 ? 4 : 2;           // words of a value load
-    static constexpr int VC = D / (16 * VW);             // loads of a value per lane
-    static constexpr int MT = D / 16;                    // 16-channel tiles of O^T
+    static constexpr int MT = D / 16;                    // 16-channel steps of S^T, tiles of O^T
     static constexpr int HB = 8 * NT;                    // heads of a block
     static constexpr int PIECE = HB * (D + 2);           // floats of a piece: o, m, l
+    static constexpr int HALF = 16 * D * 2;              // bytes of a slot: 16 keys or values
+    static constexpr int SLOTS = 3;                      // keys and values of a tile, and the next tile's keys
+    static constexpr int OROW = D + 4;                   // floats of a joined row: 2 OROW = 8 mod 32, no bank conflicts
+    static constexpr int RING = kAttnWarps * SLOTS * HALF, JOIN = kAttnWarps * HB * OROW * 4;
+    static constexpr int BODY = RING > JOIN ? RING : JOIN;  // the warps' rings, then their results
+    static constexpr int SMEM = 512 + BODY + HB * D * 2 + 2 * kAttnWarps * HB * 4;  // 512 to align the rings to a row
     // p is formed 2^7 larger for fp16, at most 2^15: small weights then keep 7 more bits above fp16's smallest step.
     // l carries the same factor, so it drops out.
     __host__ __device__ static constexpr float kLift(bool bf) { return bf ? 0.0f : 7.0f; }
-    static constexpr int SMEM = (kAttnWarps * HB * D + 2 * kAttnWarps * HB) * 4;
 };
 
+// What the 16-byte chunk number of a row in shared memory is combined with (exclusive or).
+template <int D>
+__host__ __device__ constexpr int attn_swizzle(int row) {
+    return D == 32 ? row >> 1 & 3 : row & 7;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t to, const void* from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+
 template <bool BF, int D, int NT, bool CHOSEN>
-__global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDecodeArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : D == 128 && NT == 2 ? 3 : 4) attn_decode_kernel(const AttnDecodeArgs a) {
     using S = AttnShape<D, NT>;
-    extern __shared__ __align__(16) float s_o[];         // [warp][head][D], then m and l [warp][head]
-    float* const s_m = s_o + kAttnWarps * S::HB * D;
+    extern __shared__ __align__(512) char s_raw[];       // rings or results, Q, then m and l [warp][head]
+    char* const s_body = s_raw + ((512u - (tc::smem_u32(s_raw) & 511u)) & 511u);
+    float* const s_o = reinterpret_cast<float*>(s_body);
+    char* const s_q = s_body + S::BODY;
+    float* const s_m = reinterpret_cast<float*>(s_q + S::HB * D * 2);
     float* const s_l = s_m + kAttnWarps * S::HB;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int pairs = a.Hkv * a.hblocks;                 // work rows of a row
@@ -261,21 +264,6 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
         const int32_t* list = CHOSEN ? a.pages + ((size_t)b * a.Hkv + hk) * a.n_sel : nullptr;
         const int row_pages = (len + a.page_size - 1) / a.page_size;
 
-        // Q as the B operand: lane (g, t) holds channels 32 c + 8 t ... + 7 of head g
-        uint32_t qf[NT][S::KC][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int h = 8 * n + g;
-#pragma unroll
-            for (int c = 0; c < S::KC; ++c) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (h < heads)
-                    x = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
-                                                        ((size_t)b * a.Hq + h0 + h) * D + 32 * c + 8 * t);
-                qf[n][c][0] = x.x; qf[n][c][1] = x.y; qf[n][c][2] = x.z; qf[n][c][3] = x.w;
-            }
-        }
-
         float o[NT][S::MT][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -285,80 +273,148 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
             l[n][0] = l[n][1] = 0.0f;
         }
 
-        // A tile's place: keys of the tile inside the row (0: nothing to do), and the element of its first key.
-        auto find = [&](int tile, size_t& base) -> int {
-            int page = tile / a.tiles_per_page;
-            const int off = (tile - page * a.tiles_per_page) * 16;
-            if (CHOSEN) {
-                page = list[page];
-                if (page < 0) return 0;                  // padding of the list
-                if (page >= row_pages) {
-                    if (lane == 0) raise_error(kErrPage);
-                    return 0;
-                }
+        // The warp's tiles are first + warp, + kAttnWarps, ...  Their places go through three steps, each a tile ahead of the
+        // next, so that no load of the list or of the table is waited for: the logical page, the physical one, the place.
+        struct Look {
+            int page, off, phys;  // page: -1 when the tile has no key
+        };
+        struct Tile {
+            size_t base;
+            int n;
+        };
+        int tiles_left = (last - first - warp + kAttnWarps - 1) / kAttnWarps;
+        int l_slot = (first + warp) / a.tiles_per_page, l_off = first + warp - l_slot * a.tiles_per_page;
+        const int step_pages = kAttnWarps / a.tiles_per_page, step_off = kAttnWarps - step_pages * a.tiles_per_page;
+        auto list_page = [&](Look& x) {
+            x.page = -1;
+            x.off = l_off;
+            if (tiles_left-- > 0) x.page = CHOSEN ? list[l_slot] : l_slot;
+            l_slot += step_pages;
+            l_off += step_off;
+            if (l_off >= a.tiles_per_page) {
+                l_off -= a.tiles_per_page;
+                ++l_slot;
             }
-            const int left = len - (page * a.page_size + off);
-            if (left <= 0) return 0;
-            const int phys = table[page];
-            if (phys < 0 || phys >= a.num_pages) {
+        };
+        auto look_up = [&](Look& x) {
+            if (x.page < 0) return;                      // behind the piece, or padding of the list
+            if (CHOSEN && x.page >= row_pages) {
                 if (lane == 0) raise_error(kErrPage);
-                return 0;
-            }
-            base = (((size_t)phys * a.Hkv + hk) * a.page_size + off) * D;
-            if (!in_bounds((long long)base + 16 * D - 1, (long long)a.num_pages * a.Hkv * a.page_size * D)) return 0;
-            return left < 16 ? left : 16;
-        };
-        // Keys behind the row's last one are never read: their lanes read the tile's first key instead.
-        uint32_t kf[2][S::KC][4], vf[4][S::VC][S::VW];
-        auto load_k = [&](size_t base, int n) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int key = g + 8 * i < n ? g + 8 * i : 0;
-                const uint16_t* p = reinterpret_cast<const uint16_t*>(a.k_cache) + base + key * D + 8 * t;
-#pragma unroll
-                for (int c = 0; c < S::KC; ++c) ld_stream<4>(p + 32 * c, kf[i][c]);
+                x.page = -1;
+            } else if (len <= x.page * a.page_size + x.off * 16) {
+                x.page = -1;
+            } else {
+                x.phys = table[x.page];
             }
         };
-        auto load_v = [&](size_t base, int n) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at_key = 2 * t + (i & 1) + 8 * (i >> 1);
-                const int key = at_key < n ? at_key : 0;
-                const uint16_t* p = reinterpret_cast<const uint16_t*>(a.v_cache) + base + key * D + 2 * S::VW * g;
-#pragma unroll
-                for (int c = 0; c < S::VC; ++c) ld_stream<S::VW>(p + 16 * S::VW * c, vf[i][c]);
+        auto settle = [&](const Look& x) -> Tile {
+            if (x.page < 0) return Tile{0, 0};
+            if (x.phys < 0 || x.phys >= a.num_pages) {
+                if (lane == 0) raise_error(kErrPage);
+                return Tile{0, 0};
             }
+            const size_t base = (((size_t)x.phys * a.Hkv + hk) * a.page_size + x.off * 16) * D;
+            if (!in_bounds((long long)base + 16 * D - 1, (long long)a.num_pages * a.Hkv * a.page_size * D)) return Tile{0, 0};
+            return Tile{base, min(16, len - (x.page * a.page_size + x.off * 16))};
+        };
+        // Slot `slot` of the warp's ring <- the n keys or values from element `base` on; zeros behind them.
+        constexpr int CPR = D / 8, RPI = 32 / CPR;       // 16-byte chunks of a row, rows of a copy instruction
+        const int r0 = lane / CPR, col = lane % CPR;
+        const uint32_t ring = tc::smem_u32(s_body) + warp * (S::SLOTS * S::HALF);
+        const uint32_t fill = ring + r0 * (D * 2) + ((col ^ attn_swizzle<D>(r0)) << 4);
+        auto copy = [&](const void* cache, size_t base, int n, int slot) {
+            if (n > 0) {
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(cache) + base + r0 * D + 8 * col;
+#pragma unroll
+                for (int i = 0; i < 16 / RPI; ++i)
+                    cp_async16((fill + slot * S::HALF + i * RPI * (D * 2)) ^ (attn_swizzle<D>(i * RPI) << 4), p + i * RPI * D,
+                               r0 + i * RPI < n ? 16 : 0);
+            }
+            tc::cp_async_commit();
         };
 
-        int tile = first + warp;
-        size_t base = 0;
-        int n_keys = 0;
-        auto advance = [&]() {  // the warp's next tile with a key in it
-            n_keys = 0;
-            while (tile < last && (n_keys = find(tile, base)) == 0) tile += kAttnWarps;
-        };
-        advance();
-        if (n_keys > 0) {
-            load_k(base, n_keys);
-            load_v(base, n_keys);
+        // Q is asked for before the places, which take two loads that wait for one another
+        constexpr int QN = (S::HB * CPR + kAttnThreads - 1) / kAttnThreads;
+        uint4 qx[QN];
+#pragma unroll
+        for (int u = 0; u < QN; ++u) {
+            const int i = tid + u * kAttnThreads, h = i / CPR, c = i - h * CPR;
+            qx[u] = make_uint4(0, 0, 0, 0);
+            if (h < heads)
+                qx[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + ((size_t)b * a.Hq + h0 + h) * D + 8 * c);
         }
-        while (n_keys > 0) {
-            const int n_now = n_keys;
-            tile += kAttnWarps;
-            advance();  // the next tile's place is looked up while this one's keys are on their way
-            float s[NT][4];
+        const int tiles_mine = tiles_left;
+        Look look0, look1, look2, look3;
+        list_page(look0);
+        list_page(look1);
+        list_page(look2);
+        list_page(look3);
+        look_up(look0);
+        look_up(look1);
+        look_up(look2);
+        Tile now = settle(look0);
+        copy(a.k_cache, now.base, now.n, 0);
+        copy(a.v_cache, now.base, now.n, 1);
+        Tile next = settle(look1);
+        copy(a.k_cache, next.base, next.n, 2);
+
+#pragma unroll
+        for (int u = 0; u < QN; ++u) {
+            const int i = tid + u * kAttnThreads, h = i / CPR, c = i - h * CPR;
+            if (i < S::HB * CPR) *reinterpret_cast<uint4*>(s_q + h * (D * 2) + ((c ^ attn_swizzle<D>(h)) << 4)) = qx[u];
+        }
+        __syncthreads();
+
+        // This lane's row and chunk of the first step's matrices; a step on is an exclusive or with 32 bytes, as rows are
+        // aligned to their size.
+        const int mat = lane >> 3, row = lane & 7;
+        const int k_row = row + 8 * (mat & 1), v_row = row + 8 * (mat >> 1), q_row = NT == 2 ? row + 8 * (mat >> 1) : row;
+        const uint32_t k_at = ring + k_row * (D * 2) + (((mat >> 1) ^ attn_swizzle<D>(k_row)) << 4);
+        const uint32_t v_at = ring + v_row * (D * 2) + (((mat & 1) ^ attn_swizzle<D>(v_row)) << 4);
+        const uint32_t q_at = tc::smem_u32(s_q) + q_row * (D * 2) + (((NT == 2 ? mat & 1 : mat) ^ attn_swizzle<D>(q_row)) << 4);
+
+        int slot = 0;
+        auto turn = [&]() { slot = slot + 1 == S::SLOTS ? 0 : slot + 1; };
+        for (int k = 0; k < tiles_mine; ++k) {
+            const int n_now = now.n;
+            const Tile after = settle(look2);
+            look2 = look3;
+            look_up(look2);
+            list_page(look3);
+            if (n_now == 0) {  // only the ring goes on
+                copy(a.v_cache, next.base, next.n, slot);
+                turn();
+                copy(a.k_cache, after.base, after.n, slot);
+                turn();
+                now = next;
+                next = after;
+                continue;
+            }
+            tc::cp_async_wait<S::SLOTS - 1>();
+            __syncwarp();
+            float s[NT][4], odd[NT][4];  // the odd steps' part: half as long a chain of dependent products
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
 #pragma unroll
-                for (int c = 0; c < S::KC; ++c) {
-                    const uint32_t lo[4] = {kf[0][c][0], kf[1][c][0], kf[0][c][1], kf[1][c][1]};
-                    const uint32_t hi[4] = {kf[0][c][2], kf[1][c][2], kf[0][c][3], kf[1][c][3]};
-                    wm::mma16816x<BF>(s[n], lo, qf[n][c][0], qf[n][c][1]);
-                    wm::mma16816x<BF>(s[n], hi, qf[n][c][2], qf[n][c][3]);
+                for (int e = 0; e < 4; ++e) s[n][e] = odd[n][e] = 0.0f;
+            }
+            uint32_t qf[4];
+#pragma unroll
+            for (int c = 0; c < S::MT; ++c) {
+                uint32_t kf[4];
+                wm::ldsm_x4((k_at + slot * S::HALF) ^ (c << 5), kf);
+                if constexpr (NT == 2) {
+                    wm::ldsm_x4(q_at ^ (c << 5), qf);
+                    wm::mma16816x<BF>(c % 2 ? odd[0] : s[0], kf, qf[0], qf[1]);
+                    wm::mma16816x<BF>(c % 2 ? odd[NT - 1] : s[NT - 1], kf, qf[2], qf[3]);
+                } else {  // two steps' fragments at a time
+                    if (c % 2 == 0) wm::ldsm_x4(q_at ^ (c << 5), qf);
+                    wm::mma16816x<BF>(c % 2 ? odd[0] : s[0], kf, qf[c % 2 * 2], qf[c % 2 * 2 + 1]);
                 }
             }
-            if (n_keys > 0) load_k(base, n_keys);
+            __syncwarp();
+            copy(a.v_cache, next.base, next.n, slot);
+            turn();
 
             // lane (g, t): keys g (0, 1) and g + 8 (2, 3) of heads 2 t and 2 t + 1
             bool grow = false;
@@ -366,7 +422,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[n][e] *= a.scale_log2;
+                    s[n][e] = (s[n][e] + odd[n][e]) * a.scale_log2;
                     if (g + 8 * (e >> 1) >= n_now) s[n][e] = -INFINITY;
                     grow |= s[n][e] > m[n][e & 1] + 8.0f;
                 }
@@ -406,26 +462,27 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
                     pl[n][i] = movmatrix(lo);
                 }
             }
+            tc::cp_async_wait<S::SLOTS - 1>();
+            __syncwarp();
 #pragma unroll
-            for (int c = 0; c < S::VC; ++c) {
+            for (int c = 0; c < S::MT; ++c) {
+                uint32_t vt[4];
+                wm::ldsm_x4_t((v_at + slot * S::HALF) ^ (c << 5), vt);
 #pragma unroll
-                for (int w = 0; w < S::VW; ++w) {
-                    const uint32_t vt[4] = {__byte_perm(vf[0][c][w], vf[1][c][w], 0x5410),
-                                            __byte_perm(vf[0][c][w], vf[1][c][w], 0x7632),
-                                            __byte_perm(vf[2][c][w], vf[3][c][w], 0x5410),
-                                            __byte_perm(vf[2][c][w], vf[3][c][w], 0x7632)};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        wm::mma16816x<BF>(o[n][c * S::VW + w], vt, pl[n][0], pl[n][1]);
-                        wm::mma16816x<BF>(o[n][c * S::VW + w], vt, ph[n][0], ph[n][1]);
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    wm::mma16816x<BF>(o[n][c], vt, pl[n][0], pl[n][1]);
+                    wm::mma16816x<BF>(o[n][c], vt, ph[n][0], ph[n][1]);
                 }
             }
-            if (n_keys > 0) load_v(base, n_keys);
+            __syncwarp();
+            copy(a.k_cache, after.base, after.n, slot);
+            turn();
+            now = next;
+            next = after;
         }
 
         // the warps' results side by side, then joined
-        __syncthreads();  // the previous piece's have been read
+        __syncthreads();  // every warp is through with its ring
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -433,13 +490,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
                 const int h = 8 * n + 2 * t + e;
-                float* dst = s_o + ((size_t)warp * S::HB + h) * D;
+                float* dst = s_o + (warp * S::HB + h) * S::OROW + g;
 #pragma unroll
-                for (int c = 0; c < S::VC; ++c) {
-#pragma unroll
-                    for (int w = 0; w < S::VW; ++w)
-                        *reinterpret_cast<float2*>(dst + 16 * S::VW * c + 2 * S::VW * g + 2 * w) =
-                            make_float2(o[n][c * S::VW + w][e], o[n][c * S::VW + w][e + 2]);
+                for (int c = 0; c < S::MT; ++c) {
+                    dst[16 * c] = o[n][c][e];
+                    dst[16 * c + 8] = o[n][c][e + 2];
                 }
                 if (g == 0) {
                     s_m[warp * S::HB + h] = m[n][e];
@@ -471,7 +526,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
             for (int w = 0; w < kAttnWarps; ++w) {
                 const float mw = s_m[w * S::HB + h];
                 const float f = mw == -INFINITY ? 0.0f : exp2f(mw - top);
-                const float2 x = *reinterpret_cast<const float2*>(s_o + ((size_t)w * S::HB + h) * D + c);
+                const float2 x = *reinterpret_cast<const float2*>(s_o + (w * S::HB + h) * S::OROW + c);
                 sum += f * s_l[w * S::HB + h];
                 y0 += f * x.x;
                 y1 += f * x.y;
@@ -487,6 +542,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
             }
         }
         at += last - first;
+        if (at < end) __syncthreads();  // the next piece's keys go where the results are
     }
     if (!a.by_pair && !a.alone && tid == 0) {
         a.meta[2 * cta] = starting;
@@ -496,13 +552,14 @@ __global__ void __launch_bounds__(kAttnThreads) attn_decode_kernel(const AttnDec
 
 // Joins the pieces of a (row, key head, head block) that several CTAs share: y = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
 // M = max m_i.  CTA x takes pair x (by_pair), or the pair whose first piece CTA x of the first kernel held, blockIdx.y
-// `per` heads of it, with W / per warps a head, each taking every (W / per)-th piece, BATCH of them loaded together.
-template <int D, int NT, int W>
+// `per` heads of it, blockIdx.z C channels
+// of it, with W / per warps a head, each taking every (W / per)-th piece, BATCH of them loaded together.
+template <int D, int NT, int W, int C>
 __global__ void __launch_bounds__(32 * W) attn_join_kernel(const AttnDecodeArgs a, int ctas, int per) {
     using S = AttnShape<D, NT>;
-    constexpr int E = D / 32, V = E < 4 ? E : 4;  // channels of a lane, of one load
-    constexpr int BATCH = E < 8 ? 8 : 6;
-    __shared__ float s_o[W][D], s_m[W], s_l[W];
+    constexpr int E = C / 32, V = E < 4 ? E : 4;  // channels of a lane, of one load
+    constexpr int BATCH = E <= 2 ? 12 : E < 8 ? 8 : 6;
+    __shared__ float s_o[W][C], s_m[W], s_l[W];
     tc::wait_prerequisites();
     const int held = a.meta[2 * blockIdx.x], pieces = a.meta[2 * blockIdx.x + 1];
     const int row = a.by_pair ? blockIdx.x : held, cta0 = a.by_pair ? held : blockIdx.x;
@@ -513,7 +570,8 @@ __global__ void __launch_bounds__(32 * W) attn_join_kernel(const AttnDecodeArgs 
     const int heads = min(S::HB, a.group - hb * S::HB);
     const int strides = W / per;
     const int h = blockIdx.y * per + warp % per, sub = warp / per;
-    const size_t y0 = ((size_t)b * a.Hq + hk * a.group + hb * S::HB + h) * D;
+    const int c0 = blockIdx.z * C;
+    const size_t y0 = ((size_t)b * a.Hq + hk * a.group + hb * S::HB + h) * D + c0;
     float top = -INFINITY, sum = 0.0f, y[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) y[e] = 0.0f;
@@ -534,9 +592,9 @@ __global__ void __launch_bounds__(32 * W) attn_join_kernel(const AttnDecodeArgs 
                     lsum[u] = ml.y;
 #pragma unroll
                     for (int e = 0; e < E; e += V) {
-                        if constexpr (V == 4) *reinterpret_cast<float4*>(&o[u][e]) = *reinterpret_cast<const float4*>(p + h * D + 32 * e + 4 * lane);
-                        else if constexpr (V == 2) *reinterpret_cast<float2*>(&o[u][e]) = *reinterpret_cast<const float2*>(p + h * D + 2 * lane);
-                        else o[u][e] = p[h * D + lane];
+                        if constexpr (V == 4) *reinterpret_cast<float4*>(&o[u][e]) = *reinterpret_cast<const float4*>(p + h * D + c0 + 32 * e + 4 * lane);
+                        else if constexpr (V == 2) *reinterpret_cast<float2*>(&o[u][e]) = *reinterpret_cast<const float2*>(p + h * D + c0 + 2 * lane);
+                        else o[u][e] = p[h * D + c0 + lane];
                     }
                 }
             }
@@ -574,7 +632,7 @@ __global__ void __launch_bounds__(32 * W) attn_join_kernel(const AttnDecodeArgs 
     }
     __syncthreads();
     const int c = threadIdx.x;
-    if (c >= D || h >= heads) return;
+    if (c >= C || blockIdx.y >= heads) return;
     top = s_m[0];
 #pragma unroll
     for (int w = 1; w < W; ++w) top = fmaxf(top, s_m[w]);
@@ -585,7 +643,7 @@ __global__ void __launch_bounds__(32 * W) attn_join_kernel(const AttnDecodeArgs 
         total = fmaf(f, s_l[w], total);
         yc = fmaf(f, s_o[w][c], yc);
     }
-    st1(a.y, a.y_dt, ((size_t)b * a.Hq + hk * a.group + hb * S::HB + blockIdx.y) * D + c, total == 0.0f ? 0.0f : yc / total);
+    st1(a.y, a.y_dt, ((size_t)b * a.Hq + hk * a.group + hb * S::HB + blockIdx.y) * D + c0 + c, total == 0.0f ? 0.0f : yc / total);
 }
 
 }  // namespace gdn

@@ -236,31 +236,67 @@ __global__ void __launch_bounds__(kScoreThreads, attn_score_per_sm(D)) attn_scor
         }
     };
 
-    Item now = find(at < end), next = find(at + 1 < end);
+    // The first 8 heads' queries of an item, 16 bytes at a time; heads that the group does not have are zeros.
+    constexpr int QN = (D + kScoreThreads - 1) / kScoreThreads;
+    uint4 raw[QN];
+    auto load_q = [&](const Item& it, int h0) {
+        const int heads = min(8, a.group - h0);
+#pragma unroll
+        for (int u = 0; u < QN; ++u) {
+            const int i = tid + u * kScoreThreads, h = i / (D / 8), c = 8 * (i - h * (D / 8));
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (h < heads)
+                raw[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
+                                                         ((size_t)it.b * a.Hq + it.hk * a.group + h0 + h) * D + c);
+        }
+    };
+
+    // channel 16 m + 4 t + j of head h stands at step 4 m + j, lane 4 h + t
+    auto store_q = [&]() {
+#pragma unroll
+        for (int u = 0; u < QN; ++u) {
+            const int i = tid + u * kScoreThreads, h = i / (D / 8), c0 = 8 * (i - h * (D / 8));
+            const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+            if (h < 8) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = c0 + e;
+                    const float2 f = unpack2<BF>(w[e >> 1]);
+                    s_q[c / 16 * 4 + (c & 3)][4 * h + (c >> 2 & 3)] = (double)(e & 1 ? f.y : f.x);
+                }
+            }
+        }
+    };
+
+    Item now = find(at < end);
     load(now);
+    if (at < end) load_q(now, 0);
+    Item next = find(at + 1 < end);
     int held = -1;  // the (row, key head) whose queries are in s_q
     for (; at < end; ++at) {
         float4 m[KB];
 #pragma unroll
         for (int c = 0; c < KB; ++c) m[c] = x[c];
         const Item item = now;
+        if (held != item.b * a.Hkv + item.hk || a.group > 8) {
+            if (held >= 0 && a.group > 8) load_q(item, 0);  // the last ones loaded were another part of the group
+            __syncthreads();                                // the queries before them have been read
+            held = item.b * a.Hkv + item.hk;
+            store_q();
+            __syncthreads();
+        }
         now = next;
         load(now);
+        if (at + 1 < end && a.group <= 8 && (now.b != item.b || now.hk != item.hk)) load_q(now, 0);
         next = find(at + 2 < end);
         unsigned long long best = 0;
         for (int h0 = 0; h0 < a.group; h0 += 8) {
             const int heads = min(8, a.group - h0);
-            if (held != item.b * a.Hkv + item.hk || a.group > 8) {
-                __syncthreads();  // the queries before them have been read
-                for (int i = tid; i < D * 8; i += kScoreThreads) {
-                    const int h = i / D, c = i - h * D;
-                    // channel 16 m + 4 t + j of head h stands at step 4 m + j, lane 4 h + t
-                    s_q[c / 16 * 4 + (c & 3)][4 * h + (c >> 2 & 3)] =
-                        h < heads ? (double)ld1(a.q, BF ? kBF16 : kF16, ((size_t)item.b * a.Hq + item.hk * a.group + h0 + h) * D + c)
-                                  : 0.0;
-                }
+            if (h0 > 0) {
+                load_q(item, h0);
                 __syncthreads();
-                held = item.b * a.Hkv + item.hk;
+                store_q();
+                __syncthreads();
             }
             double sum[4][2];
 #pragma unroll
