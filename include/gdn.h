@@ -457,7 +457,8 @@ gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_c
  * that holds a position in [starts[b], lens[b]) (starts int32 [B], NULL: 0),
  *   page_mean[page][hk][:] = mean of the page's keys at positions below lens[b]
  * page_mean [num_pages, Hkv, d] fp32; the other pages' rows are left as they are.  k_cache, d as in
- * gdn_attn_decode.
+ * gdn_attn_decode.  A page that several rows touch is written for each of them: it has to hold the same number
+ * of keys in all.
  */
 gdn_status_t gdn_attn_page_mean(const void* k_cache, const int32_t* page_table, const int32_t* lens,
                                 const int32_t* starts, int B, int Hkv, int d, int max_pages, int num_pages,

@@ -16,11 +16,12 @@
 // Tile.  A warp takes 16 keys at a time, S^T = K Q^T and O^T = V^T P^T by mma.sync m16n8k16: the group's
 // query heads are the 8 columns (16 in two tiles), so a group of 8 wastes nothing.  Each warp has a ring of its own in
 // shared memory, of 3 slots of 16 keys or values, which its lanes fill by 16-byte asynchronous copies, so that two slots
-// (8 KB at d = 128) a warp are under way whatever the registers hold, and nothing waits for another warp.  Chunks of a row are swizzled by the row, and ldmatrix (transposed for V) delivers the fragments without
-// bank conflicts.  Q lies there too: it would take up to 64 registers.  P goes from the accumulators to the B operand by
-// movmatrix.  Places behind the row's last key are filled with zeros instead of being read.
-// P enters as a 16-bit value and its 16-bit remainder: a single rounding (2^-9 for bf16) would add as much
-// error as the output's own rounding, and the tensor pipe has the room.
+// (8 KB at d = 128) a warp are under way whatever the registers hold, and nothing waits for another warp.  Chunks of
+// a row are swizzled by the row, and ldmatrix (transposed for V) delivers the fragments without bank conflicts.  Q lies
+// there too: it would take up to 64 registers.  P goes from the accumulators to the B operand by movmatrix.  Places
+// behind the row's last key are filled with zeros instead of being read.
+// P enters as a 16-bit value and its 16-bit remainder: a single rounding (2^-8 for bf16) would add as much
+// error as the output's own rounding, and the tensor pipe has the room (16 % busy).
 // m follows the scores lazily: it moves only when a score exceeds it by more than 8 (in log2), so p is at
 // most 2^8, and most tiles need one vote instead of a reduction over lanes and a rescale.
 #pragma once
