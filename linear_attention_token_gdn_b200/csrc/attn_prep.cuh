@@ -44,17 +44,16 @@ struct AttnPrepArgs {
 };
 
 // The two chunks of 8 channels that lane `l` of a row of d channels holds: chunk l of both halves of the rotated part,
-// or of both halves of the part behind it.  Whether they are a rotated pair.
-__device__ __forceinline__ bool attn_chunks(int l, int d, int rot, int& i0, int& j0) {
+// or of both halves of the part behind it.
+__device__ __forceinline__ void attn_chunks(int l, int d, int rot, int& i0, int& j0) {
     const int rl = rot >> 4;
     if (l < rl) {
         i0 = 8 * l;
         j0 = i0 + (rot >> 1);
-        return true;
+    } else {
+        i0 = rot + 8 * (l - rl);
+        j0 = i0 + ((d - rot) >> 1);
     }
-    i0 = rot + 8 * (l - rl);
-    j0 = i0 + ((d - rot) >> 1);
-    return false;
 }
 
 // cos and sin of 2 pi phase / 2^32, from the Taylor series about the nearest quarter turn: |x| <= pi / 4, where the
@@ -70,37 +69,50 @@ __device__ __forceinline__ void attn_turn(int phase, float& c, float& s) {
     c = __uint_as_float(__float_as_uint(c0) ^ ((quarter + 1) << 30 & 0x80000000u));
 }
 
-// cos and sin of position * inv_freq for the lane's 8 pairs.  Adding and taking away 1.5 * 2^52 rounds to whole
-// revolutions, the fused products leave the rest with one rounding, and adding 1.5 * 2^20 puts it, in units of 2^-32,
-// into the low word: three steps of the fp64 pipe and no conversion instruction, which run at a quarter of its rate and less.
-__device__ __forceinline__ void attn_angles(const double* inv_freq, int i0, bool turns, int position, float2 (&c)[4],
-                                            float2 (&s)[4]) {
-    const double p = (double)position;
-    auto turn = [&](double f, float& cu, float& su) {
-        f *= 0.15915494309189533577;
-        const double whole = __dadd_rn(__fma_rn(p, f, 0x1.8p52), -0x1.8p52);
-        attn_turn(__double2loint(__dadd_rn(__fma_rn(p, f, -whole), 0x1.8p20)), cu, su);
-    };
+// cos and sin of position * inv_freq.  Adding and taking away 1.5 * 2^52 rounds to whole revolutions, the fused products
+// leave the rest with one rounding, and adding 1.5 * 2^20 puts it, in units of 2^-32, into the low word: three steps of
+// the fp64 pipe and no conversion instruction, which run at a quarter of its rate and less.
+__device__ __forceinline__ void attn_angle(double position, double f, float& c, float& s) {
+    f *= 0.15915494309189533577;
+    const double whole = __dadd_rn(__fma_rn(position, f, 0x1.8p52), -0x1.8p52);
+    attn_turn(__double2loint(__dadd_rn(__fma_rn(position, f, -whole), 0x1.8p20)), c, s);
+}
+
+// The same for the lane's 8 pairs, when only some lanes of the row turn: lane L finds pairs P L .. P L + P - 1, and the
+// turning lanes fetch theirs.
+template <int LPR, int P>
+__device__ __forceinline__ void attn_angles_shared(const double* inv_freq, int pairs, int l, double position, unsigned mask,
+                                                   float (&c)[8], float (&s)[8]) {
+    float cp[P], sp[P];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        c[u] = make_float2(1.0f, 1.0f);
-        s[u] = make_float2(0.0f, 0.0f);
-        if (turns) {
-            const double2 f = *reinterpret_cast<const double2*>(inv_freq + i0 + 2 * u);
-            turn(f.x, c[u].x, s[u].x);
-            turn(f.y, c[u].y, s[u].y);
-        }
+    for (int j = 0; j < P; ++j) attn_angle(position, l * P + j < pairs ? inv_freq[l * P + j] : 0.0, cp[j], sp[j]);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        c[u] = __shfl_sync(mask, cp[u % P], l * (8 / P) + u / P, LPR);
+        s[u] = __shfl_sync(mask, sp[u % P], l * (8 / P) + u / P, LPR);
     }
 }
 
-__device__ __forceinline__ void attn_angles(const double* inv_freq, int i0, bool turns, int position, float (&c)[8],
+// cos and sin for the lane's 8 pairs (1 and 0 where it does not turn).  All lanes of the row call it.
+template <int LPR>
+__device__ __forceinline__ void attn_angles(const double* inv_freq, int rot, int l, int position, unsigned mask, float (&c)[8],
                                             float (&s)[8]) {
-    float2 c2[4], s2[4];
-    attn_angles(inv_freq, i0, turns, position, c2, s2);
+    const int pairs = rot >> 1;
+    const double p = (double)position;
+    if (pairs > 4 * LPR) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        c[2 * u] = c2[u].x, c[2 * u + 1] = c2[u].y;
-        s[2 * u] = s2[u].x, s[2 * u + 1] = s2[u].y;
+        for (int u = 0; u < 8; ++u) attn_angle(p, 8 * l + u < pairs ? inv_freq[8 * l + u] : 0.0, c[u], s[u]);
+    } else if (pairs > 2 * LPR) {
+        attn_angles_shared<LPR, 4>(inv_freq, pairs, l, p, mask, c, s);
+    } else if (pairs > 0) {
+        attn_angles_shared<LPR, 2>(inv_freq, pairs, l, p, mask, c, s);
+    }
+    if (8 * l >= pairs) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            c[u] = 1.0f;
+            s[u] = 0.0f;
+        }
     }
 }
 
@@ -247,7 +259,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
     const size_t x0 = (size_t)t * (size_t)(keys ? a.k_stride : a.q_stride) + (size_t)h0 * D;
     const size_t v0 = CACHE && keys ? (size_t)t * (size_t)a.v_stride + (size_t)h0 * D : 0;
     int i0, j0;
-    const bool turns = attn_chunks(l, D, a.rot, i0, j0);
+    attn_chunks(l, D, a.rot, i0, j0);
 
     AttnRow<IN> buf[U];
     auto fetch = [&](AttnRow<IN>& to, int m) {
@@ -261,17 +273,13 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
     const int position = a.positions[t];
 
     size_t dst0 = ((size_t)t * heads + h0) * D, dst_step = (size_t)step * D;  // of the first head, and to the next
+    int page = 0, phys = -1;
     if constexpr (CACHE) {
         if (position < 0) return;  // a padding token
         const int seq = attn_seq_of(a.cu, a.num_seqs, a.N, t);
         if (seq < 0) return;
-        if (keys) {
-            const int page = position / a.page_size;
-            const int phys = attn_page(a.table, a.max_pages, a.num_pages, seq, page);
-            if (phys < 0) return;
-            dst0 = (((size_t)phys * a.Hkv + h0) * a.page_size + (position - page * a.page_size)) * D;
-            dst_step = (size_t)(step * a.page_size) * D;
-        }
+        page = position / a.page_size;
+        if (keys && page < a.max_pages) phys = a.table[(size_t)seq * a.max_pages + page];  // checked behind the angles
     }
     auto put = [&](void* out, int m, const float2 (&yi)[4], const float2 (&yj)[4]) {
         const size_t o = dst0 + (size_t)m * dst_step;
@@ -285,18 +293,28 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
 
     // y_i = r (x_i ci + x_j mj), y_j = r (x_j cj + x_i si): 1 + w and the rotation in one factor each
     float2 ci[4], cj[4], si[4], mj[4];
-    attn_angles(a.inv_freq, i0, turns, position, ci, si);
     {
+        float cs[8], sn[8];
+        attn_angles<LPR>(a.inv_freq, a.rot, l, position, mask, cs, sn);
         float2 wi[4], wj[4];
         attn_weights(keys ? a.w_k : a.w_q, i0, wi);
         attn_weights(keys ? a.w_k : a.w_q, j0, wj);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            cj[u] = mul2(ci[u], wj[u]);
-            mj[u] = mul2(make_float2(-si[u].x, -si[u].y), wj[u]);
-            ci[u] = mul2(ci[u], wi[u]);
-            si[u] = mul2(si[u], wi[u]);
+            const float2 c = make_float2(cs[2 * u], cs[2 * u + 1]), s = make_float2(sn[2 * u], sn[2 * u + 1]);
+            ci[u] = mul2(c, wi[u]);
+            cj[u] = mul2(c, wj[u]);
+            si[u] = mul2(s, wi[u]);
+            mj[u] = mul2(make_float2(-s.x, -s.y), wj[u]);
         }
+    }
+    if (CACHE && keys) {
+        if (phys < 0 || phys >= a.num_pages) {
+            raise_error(kErrPage);
+            return;
+        }
+        dst0 = (((size_t)phys * a.Hkv + h0) * a.page_size + (position - page * a.page_size)) * D;
+        dst_step = (size_t)(step * a.page_size) * D;
     }
     for (int hb = 0; hb < rows; hb += U) {
 #pragma unroll
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1
     const float* w = keys ? a.w_k : a.w_q;
 
     int i0, j0;
-    const bool turns = attn_chunks(l, D, a.rot, i0, j0);
+    attn_chunks(l, D, a.rot, i0, j0);
     // 1 + w stays in shared memory (its 16 registers would spill), in the order that the lanes read it
     float dwi[8], dwj[8];
 #pragma unroll
@@ -399,7 +417,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1
             }
         }
         float cs[8], sn[8];
-        attn_angles(a.inv_freq, i0, turns, a.positions[t], cs, sn);
+        attn_angles<LPR>(a.inv_freq, a.rot, l, a.positions[t], mask, cs, sn);
         for (int hb = 0; hb < n; hb += U) {
 #pragma unroll
             for (int m = 0; m < U; ++m) {
