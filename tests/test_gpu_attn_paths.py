@@ -25,8 +25,8 @@ def ints(values):
     return torch.tensor(values, dtype=torch.int32, device="cuda")
 
 
-# Up to 256 keys (512 from 64 pairs on) a pair is one CTA's; above, pairs are cut up, and below 111 pairs (of 444
-# resident CTAs) the pieces are found by pair instead of by CTA.
+# Up to 256 keys (512 from 64 pairs on) a pair is one CTA's; above, pairs are cut up, and when they are fewer than a quarter
+# of the resident CTAs (592 at d = 128, 296 at d = 256) the pieces are found by pair instead of by CTA.
 @pytest.mark.parametrize("B,tiles", [(1, 16), (1, 17), (31, 32), (32, 32), (33, 33), (55, 33), (56, 40), (200, 33)])
 @pytest.mark.parametrize("d,Hq,dtype", [(128, 4, BF16), (256, 20, F16)])
 def test_one_cta_a_pair_or_pieces(B, tiles, d, Hq, dtype):
