@@ -427,7 +427,9 @@ gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_c
     REQUIRE_PTR(workspace, "workspace");
     REQUIRE(workspace_bytes >= gdn_attn_decode_workspace_size(Hq, Hkv, d), "workspace of %zu bytes, %zu needed",
             workspace_bytes, gdn_attn_decode_workspace_size(Hq, Hkv, d));
-    REQUIRE(!ranges_overlap(y, (long long)B * Hq * d * elem_size(y_dtype), q, (long long)B * Hq * d * 2), "y overlaps q");
+    const long long ny = (long long)B * Hq * d * elem_size(y_dtype), nc = (long long)num_pages * Hkv * page_size * d * 2;
+    REQUIRE(!ranges_overlap(y, ny, q, (long long)B * Hq * d * 2), "y overlaps q");
+    REQUIRE(!ranges_overlap(y, ny, k_cache, nc) && !ranges_overlap(y, ny, v_cache, nc), "y overlaps a cache");
     DeviceInfo dev;
     gdn_status_t r = device_info(&dev);
     if (r != GDN_OK) return r;
@@ -457,6 +459,8 @@ gdn_status_t gdn_attn_page_mean(const void* k_cache, const int32_t* page_table, 
     if (B == 0) return GDN_OK;
     REQUIRE_PTR(k_cache, "k_cache"); REQUIRE_PTR(page_table, "page_table"); REQUIRE_PTR(lens, "lens");
     REQUIRE_PTR(page_mean, "page_mean"); OPT_PTR(starts, "starts");
+    REQUIRE(!ranges_overlap(page_mean, (long long)num_pages * Hkv * d * 4, k_cache, (long long)num_pages * Hkv * page_size * d * 2),
+            "page_mean overlaps k_cache");
     DeviceInfo dev;
     gdn_status_t r = device_info(&dev);
     if (r != GDN_OK) return r;

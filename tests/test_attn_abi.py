@@ -111,6 +111,7 @@ def decode(L, **over):
     (dict(d=0), BAD), (dict(d=16), NOT_BUILT), (dict(d=96), NOT_BUILT), (dict(i=gdn.F32), NOT_BUILT), (dict(i=5), BAD),
     (dict(y_dt=5), BAD), (dict(ps=40), NOT_BUILT), (dict(ps=0), BAD), (dict(mp=0), BAD), (dict(mp=1 << 26), BAD),
     (dict(scale=float("nan")), BAD), (dict(y=at(0)), BAD), (dict(y=None), BAD), (dict(ws=None), BAD), (dict(n=4096), BAD),
+    (dict(y=at(1)), BAD), (dict(y=at(2)), BAD),
 ])
 def test_decode_refuses(L, over, status):
     assert decode(L, **over) == status
@@ -140,7 +141,7 @@ def page_mean(L, **over):
 
 @pytest.mark.parametrize("over,status", [
     (dict(kc=None), BAD), (dict(starts=MIS), BAD), (dict(B=-1), BAD), (dict(Hkv=0), BAD), (dict(d=0), BAD), (dict(d=16), NOT_BUILT),
-    (dict(i=gdn.F32), NOT_BUILT), (dict(mean=MIS), BAD), (dict(ps=17), NOT_BUILT), (dict(np=0), BAD),
+    (dict(i=gdn.F32), NOT_BUILT), (dict(mean=MIS), BAD), (dict(ps=17), NOT_BUILT), (dict(np=0), BAD), (dict(mean=at(0)), BAD),
 ])
 def test_page_mean_refuses(L, over, status):
     assert page_mean(L, **over) == status
