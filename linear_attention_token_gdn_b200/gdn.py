@@ -555,6 +555,8 @@ def attn_prep_bwd(dq_out, dk_out, q, k, w_q, w_k, positions, inv_freq, eps=1e-6,
 def attn_decode(q, k_cache, v_cache, page_table, lens, pages=None, scale=None, y_dtype=None, y=None, workspace=None):
     """gdn_attn_decode: attention of one new token per row, q [B, Hq, d], over the first lens[b] positions of the row's
     pages, or over the listed logical pages [B, Hkv, n_sel] of each key head.  scale defaults to d ** -0.5.  Returns y."""
+    if pages is not None and pages.shape[-1] == 0:  # its address is NULL, which stands for all pages
+        raise ValueError(f"pages has room for no page: {list(pages.shape)}")
     B, Hq, d = q.shape
     num_pages, Hkv, page_size, _ = k_cache.shape
     max_pages, dev = page_table.shape[1], q.device
