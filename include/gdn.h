@@ -406,7 +406,8 @@ gdn_status_t gdn_attn_prep(const void* q, const void* k, int64_t q_stride, int64
  *   q_out [N,Hq,d], k_cache, v_cache: out_dtype (BF16 or F16; F32 returns GDN_ERR_UNSUPPORTED).
  * A token with a negative position is padding, a token at index >= cu_seqlens[num_seqs] is in no
  * sequence: neither has anything written, in q_out or in the caches.  Two tokens of a call must not
- * have the same place in the cache.
+ * have the same place in the cache.  cu_seqlens that do not begin at 0, fall or end behind N are flagged in the device error
+ * word; tokens may then have gone to pages of another of the call's sequences.
  */
 gdn_status_t gdn_attn_prep_cache(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                                  int64_t v_stride, const float* w_q, const float* w_k, float eps,

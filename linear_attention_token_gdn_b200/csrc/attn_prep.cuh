@@ -221,8 +221,17 @@ __device__ __forceinline__ int attn_page(const int32_t* table, int max_pages, in
     return phys;
 }
 
-// Sequence that token t belongs to, -1 past the last one.  Offsets out of order are flagged by the
-// range test of the found sequence.
+// Flags offsets that do not begin at 0, fall, or end behind N; thread `i` of `threads` looks at every threads-th sequence.
+// The search for a token's sequence meets a few of the offsets only, and cannot tell that the others are in order.
+__device__ __forceinline__ void attn_check_seqlens(const int32_t* cu, int num_seqs, int N, unsigned i, unsigned threads) {
+    for (long long s = i; s < num_seqs; s += threads) {
+        const int start = cu[s], end = cu[s + 1];
+        if (end < start || (s == 0 && start != 0) || (s == num_seqs - 1 && end > N)) raise_error(kErrSeqlens);
+    }
+}
+
+// Sequence that token t belongs to, -1 past the last one.  Of offsets out of order (attn_check_seqlens flags them) it names
+// a sequence that begins at or before t and ends behind it, or none.
 __device__ __forceinline__ int attn_seq_of(const int32_t* cu, int num_seqs, int N, int t) {
     if (cu == nullptr) return t / (N / num_seqs);
     if (t >= cu[num_seqs]) return -1;
@@ -250,7 +259,8 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
     const unsigned mask = attn_row_mask<LPR>();
     // The queries' units, then the keys'.  A token's units stand side by side and take every `step`-th head, so that
     // what is under way at a time is contiguous.
-    unsigned unit = (blockIdx.x * (unsigned)kAttnPrepThreads + threadIdx.x) / LPR;
+    const unsigned thread = blockIdx.x * (unsigned)kAttnPrepThreads + threadIdx.x;
+    unsigned unit = thread / LPR;
     const bool keys = unit >= (unsigned)a.N * (unsigned)a.cq;
     if (keys) unit -= (unsigned)a.N * (unsigned)a.cq;
     const int heads = keys ? a.Hkv : a.Hq, step = keys ? a.ck : a.cq;
@@ -278,6 +288,8 @@ __global__ void __launch_bounds__(kAttnPrepThreads, IN == kF32 ? 1 : 2) attn_pre
     size_t dst0 = ((size_t)t * heads + h0) * D, dst_step = (size_t)step * D;  // of the first head, and to the next
     int page = 0, phys = -1;
     if constexpr (CACHE) {
+        // behind the rows' loads and the position's, so that it waits along with them
+        if (a.cu != nullptr) attn_check_seqlens(a.cu, a.num_seqs, a.N, thread, (unsigned)a.N * (unsigned)(a.cq + a.ck) * LPR);
         if (position < 0) return;  // a padding token
         const int seq = attn_seq_of(a.cu, a.num_seqs, a.N, t);
         if (seq < 0) return;

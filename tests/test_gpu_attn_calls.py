@@ -1,5 +1,5 @@
-"""The attention operators called in ways that the documentation allows or names an error: lists that do not
-fit."""
+"""The attention operators called in ways that the documentation allows or names an error: lists and offsets that
+do not fit."""
 import pytest
 import torch
 
@@ -17,6 +17,10 @@ def _lib(cuda_device):
     gdn.lib()
 
 
+def ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
 def test_an_empty_list_of_pages_is_refused():
     """[B, Hkv, 0] is a list without a place, not the absence of a list."""
     kc, vc, table, lens = cache(1, [40, 17], 2, 64, 16, BF16)
@@ -26,3 +30,48 @@ def test_an_empty_list_of_pages_is_refused():
     none = torch.full((2, 2, 1), -1, dtype=torch.int32, device="cuda")  # a list without a page: zeros
     assert not gdn.attn_decode(q, kc, vc, table, lens, pages=none).any()
     gdn.check_device_error()
+
+
+def fill_cache(cu, N, Hq=2, Hkv=2, d=64):
+    """Tokens 0 .. N - 1 at positions 0 .. N - 1 of sequences with a page of 16 places each."""
+    g, num_seqs = gen(2), len(cu) - 1
+    q, k, v = (normal(g, N, h, d, dtype=BF16) for h in (Hq, Hkv, Hkv))
+    w = torch.zeros(d, device="cuda")
+    kc, vc = (torch.zeros(num_seqs, Hkv, 16, d, device="cuda", dtype=BF16) for _ in range(2))
+    table = torch.arange(num_seqs, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    gdn.attn_prep_cache(q, k, v, w, w, torch.arange(N, dtype=torch.int32, device="cuda"), None, kc, vc, table, cu_seqlens=ints(cu))
+    return v, vc
+
+
+MALFORMED = [[0, 6, 2, 8], [0, 5, 3], [-4, 3, 8], [0, 4, 12], [3, 5, 8], [2, 8], [0, -1, 8], [0, 8, 7], [0, 9, 8]]
+
+
+@pytest.mark.parametrize("cu", MALFORMED, ids=str)
+def test_the_cache_form_flags_malformed_offsets(cu):
+    fill_cache(cu, 8)
+    with pytest.raises(gdn.GDNError) as e:
+        gdn.check_device_error()
+    assert e.value.status == gdn.GDN_ERR_INVALID_ARG and "cu_seqlens" in str(e.value)
+    gdn.check_device_error()  # cleared
+
+
+@pytest.mark.parametrize("at,value", [(0, 1), (1, -1), (650, 2), (699, -3), (700, 2)])
+def test_the_cache_form_checks_every_offset_of_many_sequences(at, value):
+    """One token with one query and one key head of 16 channels: two threads look at 700 sequences."""
+    cu = [0] * 300 + [1] * 401
+    fill_cache(cu, 1, 1, 1, 16)
+    gdn.check_device_error()
+    cu[at] = value
+    fill_cache(cu, 1, 1, 1, 16)
+    with pytest.raises(gdn.GDNError):
+        gdn.check_device_error()
+
+
+@pytest.mark.parametrize("cu", [[0, 8], [0, 0, 8], [0, 8, 8, 8], [0, 3, 3, 5], [0, 0], [0, 0, 0, 1, 1, 7]], ids=str)
+def test_the_cache_form_takes_empty_sequences_and_tokens_behind_the_last(cu):
+    v, vc = fill_cache(cu, 8)
+    gdn.check_device_error()
+    for b in range(len(cu) - 1):
+        places = set(range(cu[b], cu[b + 1]))
+        for p in range(16):
+            assert torch.equal(vc[b, :, p], v[p]) if p in places else not vc[b, :, p].any()
