@@ -404,18 +404,23 @@ def out_gate(y, z, norm_w, eps=1e-6, out=None, stream=None):
 
 
 def _on_stream(fn):
-    """Runs ``fn`` with the first tensor's device current and, where one is given, ``stream`` as its current
+    """Runs ``fn`` with its first tensor's device current and, where one is given, ``stream`` as its current
     stream, so that what it allocates and launches belongs to that stream."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kwargs):
+    def call(*args, stream=None, **kwargs):
+        first = args[0] if args else kwargs.get(name)
+        if first is None:
+            raise TypeError(f"{fn.__name__}() needs a tensor as its argument '{name}'")
         if not first.is_cuda:
             raise ValueError("libgdn takes device tensors only")
         if stream is None and first.get_device() == torch._C._cuda_getDevice():
-            return fn(first, *args, **kwargs)
+            return fn(*args, **kwargs)
         if stream is not None and stream.device != first.device:
             raise ValueError(f"a stream of {stream.device} for tensors on {first.device}")
         with torch.cuda.device(first.device), torch.cuda.stream(stream):
-            return fn(first, *args, **kwargs)
+            return fn(*args, **kwargs)
     return call
 
 

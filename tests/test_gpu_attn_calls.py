@@ -1,9 +1,9 @@
 """The attention operators called in ways that the documentation allows or names an error: lists and offsets that
-do not fit."""
+do not fit, arguments by name."""
 import pytest
 import torch
 
-from attn_cases import cache, gen, normal
+from attn_cases import cache, frequencies, gen, normal
 from linear_attention_token_gdn_b200 import build as gbuild
 from linear_attention_token_gdn_b200 import gdn
 
@@ -75,3 +75,30 @@ def test_the_cache_form_takes_empty_sequences_and_tokens_behind_the_last(cu):
         places = set(range(cu[b], cu[b + 1]))
         for p in range(16):
             assert torch.equal(vc[b, :, p], v[p]) if p in places else not vc[b, :, p].any()
+
+
+def test_every_argument_by_name():
+    B, Hq, Hkv, d, page = 3, 4, 2, 64, 16
+    kc, vc, table, lens = cache(4, [40, 7, 100], Hkv, d, page, BF16)
+    g, f, pos = gen(4), frequencies(64), ints([39, 6, 99])
+    q, k, v = (normal(g, B, h, d, dtype=BF16) for h in (Hq, Hkv, Hkv))
+    wq, wk = normal(g, d), normal(g, d)
+    same = lambda a, b: all(torch.equal(x, y) for x, y in zip(a, b))  # noqa: E731
+    assert same(gdn.attn_prep(q=q, k=k, w_q=wq, w_k=wk, positions=pos, inv_freq=f), gdn.attn_prep(q, k, wq, wk, pos, f))
+    a = gdn.attn_prep_bwd(dq_out=q, dk_out=k, q=q, k=k, w_q=wq, w_k=wk, positions=pos, inv_freq=f)
+    assert same(a.values(), gdn.attn_prep_bwd(q, k, q, k, wq, wk, pos, f).values())
+    kc2, vc2 = kc.clone(), vc.clone()
+    a = gdn.attn_prep_cache(q=q, k=k, v=v, w_q=wq, w_k=wk, positions=pos, inv_freq=f, k_cache=kc2, v_cache=vc2, page_table=table)
+    assert torch.equal(a, gdn.attn_prep_cache(q, k, v, wq, wk, pos, f, kc, vc, table))
+    mean = gdn.attn_page_mean(k_cache=kc, page_table=table, lens=lens)
+    assert torch.equal(mean, gdn.attn_page_mean(kc, table, lens))
+    pages = gdn.attn_select(q=q, page_mean=mean, page_table=table, lens=lens, page_size=page, n_sel=3)
+    assert torch.equal(pages, gdn.attn_select(q, mean, table, lens, page, 3))
+    y = gdn.attn_decode(q=q, k_cache=kc, v_cache=vc, page_table=table, lens=lens, pages=pages)
+    assert torch.equal(y, gdn.attn_decode(q, kc, vc, table, lens, pages=pages))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    z = gdn.attn_decode(q=q, k_cache=kc, v_cache=vc, page_table=table, lens=lens, pages=pages, stream=side)
+    side.synchronize()
+    assert torch.equal(y, z)
+    gdn.check_device_error()
