@@ -1,5 +1,5 @@
 """The attention operators called in ways that the documentation allows or names an error: lists and offsets that
-do not fit, arguments by name."""
+do not fit, arguments by name, new memory as torch's settings want it."""
 import pytest
 import torch
 
@@ -102,3 +102,25 @@ def test_every_argument_by_name():
     side.synchronize()
     assert torch.equal(y, z)
     gdn.check_device_error()
+
+
+def test_new_outputs_are_filled_as_the_deterministic_setting_wants():
+    """torch fills new memory with NaN under deterministic algorithms; a padding token's row of q_out is such memory."""
+    g = gen(5)
+    q, k, v = (normal(g, 2, h, 64, dtype=BF16) for h in (4, 2, 2))
+    w, pos = torch.zeros(64, device="cuda"), ints([3, -1])
+    kc, vc = (torch.zeros(2, 2, 16, 64, device="cuda", dtype=BF16) for _ in range(2))
+    table = ints([[0], [1]])
+    call = lambda: gdn.attn_prep_cache(q, k, v, w, w, pos, None, kc, vc, table)  # noqa: E731
+    want = call()[0].clone()
+    torch.cuda.synchronize()
+    before = torch.are_deterministic_algorithms_enabled(), torch.is_deterministic_algorithms_warn_only_enabled()
+    torch.use_deterministic_algorithms(True)
+    try:
+        old = torch.full((2, 4, 64), 3.0, device="cuda", dtype=BF16)  # what the new output's memory may hold
+        del old
+        got = call()
+    finally:
+        torch.use_deterministic_algorithms(before[0], warn_only=before[1])
+    gdn.check_device_error()
+    assert torch.equal(got[0], want) and got[1].isnan().all()
