@@ -1,6 +1,8 @@
 // attn_api.cuh -- the C ABI of the attention operators (declared in include/gdn.h): argument checks and
 // launches.  Included by gdn_lib.cu, whose error reporting it uses.
 #pragma once
+#include <initializer_list>
+
 #include "attn_decode.cuh"
 #include "attn_page.cuh"
 #include "attn_prep.cuh"
@@ -37,6 +39,28 @@ long long elem_size(int dt) { return dt == GDN_F32 ? 4 : 2; }
 long long span_bytes(long long n, long long stride, long long width, int dt) {
     return n > 0 ? ((n - 1) * stride + width) * elem_size(dt) : 0;
 }
+
+struct Range {
+    const char* name;
+    const void* p;
+    long long bytes;
+};
+
+// No output on an input, nor on another output.
+gdn_status_t require_apart(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+    for (const Range* a = outs.begin(); a != outs.end(); ++a) {
+        for (const Range* b = a + 1; b != outs.end(); ++b)
+            REQUIRE(!ranges_overlap(a->p, a->bytes, b->p, b->bytes), "%s overlaps %s", a->name, b->name);
+        for (const Range& b : ins) REQUIRE(!ranges_overlap(a->p, a->bytes, b.p, b.bytes), "%s overlaps %s", a->name, b.name);
+    }
+    return GDN_OK;
+}
+
+#define REQUIRE_APART(...)                                     \
+    do {                                                       \
+        const gdn_status_t apart = require_apart(__VA_ARGS__); \
+        if (apart != GDN_OK) return apart;                     \
+    } while (0)
 
 #define REQUIRE_ATTN_HEADS()                                                                              \
     do {                                                                                                  \
@@ -262,10 +286,12 @@ gdn_status_t gdn_attn_prep(const void* q, const void* k, int64_t q_stride, int64
     const long long sk = span_bytes(N, k_stride, (long long)Hkv * d, in_dtype);
     const bool q_in_place = q_out == q && q_stride == (int64_t)Hq * d && in_dtype == out_dtype;
     const bool k_in_place = k_out == k && k_stride == (int64_t)Hkv * d && in_dtype == out_dtype;
-    REQUIRE(!ranges_overlap(q_out, nq, k_out, nk), "q_out overlaps k_out");
     REQUIRE((q_in_place || !ranges_overlap(q_out, nq, q, sq)) && !ranges_overlap(q_out, nq, k, sk) &&
                 (k_in_place || !ranges_overlap(k_out, nk, k, sk)) && !ranges_overlap(k_out, nk, q, sq),
             "an output overlaps an input");
+    REQUIRE_APART({{"q_out", q_out, nq}, {"k_out", k_out, nk}},
+                  {{"w_q", w_q, 4LL * d}, {"w_k", w_k, 4LL * d}, {"positions", positions, 4LL * N},
+                   {"inv_freq", inv_freq, 4LL * rot_dim}});
     gdn::AttnPrepArgs a{};
     a.q = q; a.k = k; a.v = nullptr; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = 0;
     a.w_q = w_q; a.w_k = w_k; a.eps = eps; a.positions = positions; a.inv_freq = inv_freq; a.rot = rot_dim;
@@ -306,12 +332,11 @@ gdn_status_t gdn_attn_prep_cache(const void* q, const void* k, const void* v, in
     REQUIRE((in_place || !ranges_overlap(q_out, nq, q, sq)) && !ranges_overlap(q_out, nq, k, sk) &&
                 !ranges_overlap(q_out, nq, v, sv),
             "q_out overlaps an input");
-    const void* caches[2] = {k_cache, v_cache};
-    for (const void* c : caches)
-        REQUIRE(!ranges_overlap(c, nc, q, sq) && !ranges_overlap(c, nc, k, sk) && !ranges_overlap(c, nc, v, sv) &&
-                    !ranges_overlap(c, nc, q_out, nq),
-                "a cache overlaps another tensor");
-    REQUIRE(!ranges_overlap(k_cache, nc, v_cache, nc), "k_cache overlaps v_cache");
+    REQUIRE_APART({{"q_out", q_out, nq}, {"k_cache", k_cache, nc}, {"v_cache", v_cache, nc}},
+                  {{"w_q", w_q, 4LL * d}, {"w_k", w_k, 4LL * d}, {"positions", positions, 4LL * N},
+                   {"inv_freq", inv_freq, 4LL * rot_dim}, {"cu_seqlens", cu_seqlens, 4LL * num_seqs + 4},
+                   {"page_table", page_table, 4LL * num_seqs * max_pages}});
+    REQUIRE_APART({{"k_cache", k_cache, nc}, {"v_cache", v_cache, nc}}, {{"q", q, sq}, {"k", k, sk}, {"v", v, sv}});
     gdn::AttnPrepArgs a{};
     a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
     a.w_q = w_q; a.w_k = w_k; a.eps = eps; a.positions = positions; a.inv_freq = inv_freq; a.rot = rot_dim;
@@ -355,14 +380,10 @@ gdn_status_t gdn_attn_prep_bwd(const void* dq_out, const void* dk_out, const voi
     const long long gq = (long long)N * Hq * d * elem_size(dy_dtype), gk = (long long)N * Hkv * d * elem_size(dy_dtype);
     const long long sq = span_bytes(N, q_stride, (long long)Hq * d, in_dtype);
     const long long sk = span_bytes(N, k_stride, (long long)Hkv * d, in_dtype);
-    const void* outs[2] = {dq, dk};
-    for (int i = 0; i < 2; ++i) {
-        const long long n = i == 0 ? oq : ok;
-        REQUIRE(!ranges_overlap(outs[i], n, dq_out, gq) && !ranges_overlap(outs[i], n, dk_out, gk) &&
-                    !ranges_overlap(outs[i], n, q, sq) && !ranges_overlap(outs[i], n, k, sk),
-                "an output overlaps an input");
-    }
-    REQUIRE(!ranges_overlap(dq, oq, dk, ok), "dq overlaps dk");
+    REQUIRE_APART({{"dq", dq, oq}, {"dk", dk, ok}, {"dw_q", dw_q, 4LL * d}, {"dw_k", dw_k, 4LL * d},
+                   {"workspace", workspace, (long long)gdn_attn_prep_bwd_workspace_size(d)}},
+                  {{"dq_out", dq_out, gq}, {"dk_out", dk_out, gk}, {"q", q, sq}, {"k", k, sk}, {"w_q", w_q, 4LL * d},
+                   {"w_k", w_k, 4LL * d}, {"positions", positions, 4LL * N}, {"inv_freq", inv_freq, 4LL * rot_dim}});
     DeviceInfo dev;
     gdn_status_t r = device_info(&dev);
     if (r != GDN_OK) return r;
