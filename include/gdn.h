@@ -373,6 +373,7 @@ gdn_status_t gdn_state_map_apply(const float* M, const float* B, const float* S_
  * Errors.   A table entry outside [0, num_pages), a position or length beyond the table, or a
  *           listed page beyond the row's length is skipped and flagged in the device error word
  *           (gdn_check_device_error then returns GDN_ERR_INVALID_ARG).
+ * Overlaps. Outputs and workspaces lie on no input and on no other output; what a call says it may do in place excepted.
  * Workspace. A workspace serves one call at a time: calls that may overlap on the GPU (two streams,
  *           two graphs) need one each.
  */

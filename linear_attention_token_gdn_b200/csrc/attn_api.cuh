@@ -449,8 +449,10 @@ gdn_status_t gdn_attn_decode(const void* q, const void* k_cache, const void* v_c
     REQUIRE(workspace_bytes >= gdn_attn_decode_workspace_size(Hq, Hkv, d), "workspace of %zu bytes, %zu needed",
             workspace_bytes, gdn_attn_decode_workspace_size(Hq, Hkv, d));
     const long long ny = (long long)B * Hq * d * elem_size(y_dtype), nc = (long long)num_pages * Hkv * page_size * d * 2;
-    REQUIRE(!ranges_overlap(y, ny, q, (long long)B * Hq * d * 2), "y overlaps q");
-    REQUIRE(!ranges_overlap(y, ny, k_cache, nc) && !ranges_overlap(y, ny, v_cache, nc), "y overlaps a cache");
+    REQUIRE_APART({{"y", y, ny}, {"workspace", workspace, (long long)gdn_attn_decode_workspace_size(Hq, Hkv, d)}},
+                  {{"q", q, (long long)B * Hq * d * 2}, {"k_cache", k_cache, nc}, {"v_cache", v_cache, nc},
+                   {"page_table", page_table, 4LL * B * max_pages}, {"lens", lens, 4LL * B},
+                   {"pages", pages, 4LL * B * Hkv * n_sel}});
     DeviceInfo dev;
     gdn_status_t r = device_info(&dev);
     if (r != GDN_OK) return r;
@@ -480,8 +482,9 @@ gdn_status_t gdn_attn_page_mean(const void* k_cache, const int32_t* page_table, 
     if (B == 0) return GDN_OK;
     REQUIRE_PTR(k_cache, "k_cache"); REQUIRE_PTR(page_table, "page_table"); REQUIRE_PTR(lens, "lens");
     REQUIRE_PTR(page_mean, "page_mean"); OPT_PTR(starts, "starts");
-    REQUIRE(!ranges_overlap(page_mean, (long long)num_pages * Hkv * d * 4, k_cache, (long long)num_pages * Hkv * page_size * d * 2),
-            "page_mean overlaps k_cache");
+    REQUIRE_APART({{"page_mean", page_mean, (long long)num_pages * Hkv * d * 4}},
+                  {{"k_cache", k_cache, (long long)num_pages * Hkv * page_size * d * 2},
+                   {"page_table", page_table, 4LL * B * max_pages}, {"lens", lens, 4LL * B}, {"starts", starts, 4LL * B}});
     DeviceInfo dev;
     gdn_status_t r = device_info(&dev);
     if (r != GDN_OK) return r;
@@ -518,6 +521,10 @@ gdn_status_t gdn_attn_select(const void* q, const float* page_mean, const int32_
     REQUIRE_PTR(lens, "lens"); REQUIRE_PTR(pages, "pages"); REQUIRE_PTR(workspace, "workspace");
     REQUIRE(workspace_bytes >= gdn_attn_select_workspace_size(B, Hkv, max_pages), "workspace of %zu bytes, %zu needed",
             workspace_bytes, gdn_attn_select_workspace_size(B, Hkv, max_pages));
+    REQUIRE_APART({{"pages", pages, 4LL * B * Hkv * n_sel},
+                   {"workspace", workspace, (long long)gdn_attn_select_workspace_size(B, Hkv, max_pages)}},
+                  {{"q", q, (long long)B * Hq * d * 2}, {"page_mean", page_mean, (long long)num_pages * Hkv * d * 4},
+                   {"page_table", page_table, 4LL * B * max_pages}, {"lens", lens, 4LL * B}});
     DeviceInfo dev;
     gdn_status_t r = device_info(&dev);
     if (r != GDN_OK) return r;
