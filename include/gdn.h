@@ -359,9 +359,10 @@ gdn_status_t gdn_state_map_apply(const float* M, const float* B, const float* S_
  * The attention layer's operators
  * -------------------------------
  * The architecture keeps one attention layer after every third GDN mixer.  The calls below are
- * that layer's parts: the norms and the position rotation of its queries and keys (with their
- * gradients, and in the form that fills a paged cache), the attention of one new token per row
- * over that cache, and the choice of the cache pages that such a token attends to.
+ * parts of that layer: the norms and the position rotation of its queries and keys (with their
+ * gradients, and in the form that fills a paged cache), and the attention of one new token per row
+ * over that cache.  The choice of the cache pages that such a token attends to is this library's
+ * own definition, stated at gdn_attn_select; it is not the indexer of the architecture's sparse attention.
  *
  * Heads.    Hq query heads and Hkv key heads, Hq a multiple of Hkv: query head h reads key head
  *           h / (Hq / Hkv).
@@ -384,7 +385,7 @@ gdn_status_t gdn_state_map_apply(const float* M, const float* B, const float* S_
  *   n_i = x_i / sqrt(mean_j x_j^2 + eps) * (1 + w_i),   theta_i = positions[t] * inv_freq[i]
  *   y_i = n_i cos theta_i - n_{i+rot_dim/2} sin theta_i     (i < rot_dim / 2)
  *   y_{i+rot_dim/2} = n_{i+rot_dim/2} cos theta_i + n_i sin theta_i
- * and y_i = n_i for i >= rot_dim.
+ * and y_i = n_i for i >= rot_dim.  Sums are fp32: the squares of a row have to add up within its range (|x| below 2^60).
  *   q [N,Hq,d], k [N,Hkv,d]: in_dtype; a token's heads contiguous, tokens q_stride and k_stride
  *     elements apart (multiples of 8), so both may be slices of one projection's output.
  *   w_q, w_k [d] fp32.  positions int32 [N].  inv_freq [rot_dim / 2] fp64, radians per position

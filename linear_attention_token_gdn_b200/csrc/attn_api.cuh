@@ -169,10 +169,18 @@ bool attn_head_dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128 
 
 // ---------------------------------------------------------------- decode
 
-// Whether a pair is left to one CTA, given the most tiles of 16 keys that it can have: up to 256 keys always, up to 512
-// when there are 64 pairs and more.  Measured (us, one CTA a pair against pieces and a join; d = 128): 1 row of 2 key heads,
-// 256 keys 7.7 / 8.5, 512 keys 10.8 / 8.3; 8 rows of 8 key heads, 512 keys 10.8 / 15.9, 1024 keys 21.5 / 18.6; 64 rows of 8,
-// 512 keys 27.8 / 28.6, 1024 keys 47.0 / 40.6.
+// Whether a pair is left to one CTA, given the most tiles of 16 keys that it can have (by the page table's width: the lengths are
+// on the device): up to 256 keys always, up to 512 when there are 64 pairs and more.  Measured in a graph (us, one CTA a pair
+// against pieces and a join; bf16, groups of 4, equal rows):
+//   rows x key heads    keys     d = 32        64           128          256
+//        1 x 2           256   3.9 /  5.7   4.1 /  5.8    5.2 /  6.5    6.7 /  7.3
+//                        512   5.3 /  5.9   5.6 /  5.9    7.5 /  6.7   10.0 /  7.7
+//        8 x 8           512   7.1 /  9.3   7.5 / 12.5    9.1 / 13.7   11.8 / 16.5
+//                       1024  10.8 / 10.1  11.6 / 13.9   14.4 / 16.7   18.9 / 22.3
+//       64 x 8           512  10.1 / 15.3  15.2 / 20.8   27.2 / 33.0   47.5 / 52.5
+//                       1024  16.2 / 21.0  25.8 / 32.0   45.9 / 53.0   82.3 / 90.9
+// Equal rows of 1024 keys would still gain from one CTA a pair at 64 pairs and more; the limit stays below, as one long row among
+// short ones would then be alone on its CTA.  Rows of 256 keys under a table for many more are cut: 8 x 8 of 128, 12.0 for 6.4.
 bool attn_alone(long long tiles, long long pairs) { return tiles <= (pairs >= 64 ? 32 : 16); }
 
 template <bool BF, int D, int NT, bool CHOSEN>

@@ -4,7 +4,8 @@
 //   mean_p = sum of the page's keys inside the row's length / their count            (fp32)
 //   score_p = max over the query heads h of the key head's group of q_h . mean_p      (fp64)
 // The first n_first and the last n_last pages are always chosen, the rest by score, ties to the lower page;
-// the list is ascending, -1 behind its end.
+// the list is ascending, -1 behind its end.  The score is this library's own; the architecture's sparse attention has an indexer
+// of its own, which this is not.
 //
 // Scores are summed in fp64: which page is the last to be chosen can hang on the last bits of two scores,
 // and with 2^-53 the order of the sum (so the tile, or another build) no longer decides it in practice.
@@ -177,7 +178,7 @@ __device__ __forceinline__ void dmma(double (&c)[2], double a, double b) {
 // only the queries do, as doubles in fragment order, once per (row, key head).  The next pages' means load under this
 // one's products, their places in the cache having been looked up one step earlier; four independent sums keep a step's
 // products from waiting for one another.  What bounds it: HBM (the means), the products
-// (8.5 us below) and the conversions to fp64, 16 a clock and SM.  Measured: 16,800 pages of 64 rows, 8 key heads of 128,
+// (8.5 us below) and the conversions to fp64, 16 a clock and SM.  12 bytes a thread spill at d = 64 and 128.  Measured: 16,800 pages of 64 rows, 8 key heads of 128,
 // groups of 4: 22 us (means through shared memory and fused multiply-adds: 95); 7900 pages of 4 rows, 4 key heads: 11 us.
 template <bool BF, int D>
 __global__ void __launch_bounds__(kScoreThreads, attn_score_per_sm(D)) attn_score_kernel(const AttnSelectArgs a) {
